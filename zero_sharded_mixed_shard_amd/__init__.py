@@ -97,6 +97,22 @@ from ._binding import (  # noqa: F401
     zero_shard_layout,
     zero_strerror,
 )
+from ._grad import (  # noqa: F401
+    ACT_BLOCK,
+    ACT_GELU,
+    ACT_NONE,
+    ACT_SILU,
+    zero_act_backward,
+    zero_act_load,
+    zero_act_save,
+    zero_embed_grad,
+    zero_embed_grad_workspace,
+    zero_embed_lookup,
+    zero_policy_loss,
+    zero_policy_loss_dev,
+    zero_weight_grad,
+    zero_weight_grad_workspace,
+)
 
 __all__ = [
     "Layout",
@@ -141,4 +157,18 @@ __all__ = [
     "layout",
     "overflow_check",
     "adam_step",
+    "ACT_BLOCK",
+    "ACT_GELU",
+    "ACT_NONE",
+    "ACT_SILU",
+    "zero_act_backward",
+    "zero_act_load",
+    "zero_act_save",
+    "zero_embed_grad",
+    "zero_embed_grad_workspace",
+    "zero_embed_lookup",
+    "zero_policy_loss",
+    "zero_policy_loss_dev",
+    "zero_weight_grad",
+    "zero_weight_grad_workspace",
 ]

@@ -19,6 +19,7 @@ import re
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,13 +28,13 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libzero_shard.so")
 # SHA-256 of each kernel's machine code, written beside the library by build()
 ISA_HASHES = os.path.join(PKG, "kernel_isa.sha256")
-KERNEL_SOURCES = ["shard_kernels.hip", "exchange_kernels.hip"]
+KERNEL_SOURCES = ["shard_kernels.hip", "exchange_kernels.hip", "act_kernels.hip",
+                  "wgrad_kernels.hip", "embed_kernels.hip", "policy_kernels.hip"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["layout.cpp", "scaler.cpp", "accounting.cpp", "checkpoint.cpp", "api.cpp",
-           "shard_kernels.hip",
-           "exchange_kernels.hip"]
+           "grad_api.cpp", *KERNEL_SOURCES]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-ffp-contract=off",
           f"-I{INCLUDE}", f"-I{CSRC}"]
 DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -49,24 +50,24 @@ def _run(cmd):
 
 def build(verbose: bool = False) -> str:
     """Compile every source for gfx950 and link the shared library."""
-    with tempfile.TemporaryDirectory() as tmp:
-        objs = []
-        for src in SOURCES:
-            obj = os.path.join(tmp, src + ".o")
-            # every source goes through the HIP driver (host files include the runtime API)
-            cmd = [HIPCC, "-x", "hip", *DEVICE, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
-            if verbose:
-                print(" ".join(cmd))
-            _run(cmd)
-            objs.append(obj)
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(max_workers=4) as pool:
+        objs = [os.path.join(tmp, src + ".o") for src in SOURCES]
+        # every source goes through the HIP driver (host files include the runtime API)
+        cmds = [[HIPCC, "-x", "hip", *DEVICE, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
+                for src, obj in zip(SOURCES, objs)]
+        if verbose:
+            print("\n".join(" ".join(cmd) for cmd in cmds))
+        assembly = pool.map(device_assembly, KERNEL_SOURCES)   # beside the compiles
+        for _ in pool.map(_run, cmds):
+            pass
         out_tmp = LIB + ".tmp"
         cmd = [HIPCC, *DEVICE, "-shared", "-fPIC", "-o", out_tmp, *objs]
         if verbose:
             print(" ".join(cmd))
         _run(cmd)
         hashes = {}
-        for src in KERNEL_SOURCES:
-            hashes.update(kernel_isa_hashes(device_assembly(src)))
+        for text in assembly:
+            hashes.update(kernel_isa_hashes(text))
         with open(ISA_HASHES + ".tmp", "w") as f:
             for name in sorted(hashes):
                 f.write(f"{hashes[name]}  {name}\n")

@@ -17,11 +17,7 @@ namespace {
 
 thread_local char g_err[256];
 
-int fail_hip(hipError_t e, const char *what) {
-    std::snprintf(g_err, sizeof g_err, "HIP error in %s: %s (%d)", what, hipGetErrorString(e),
-                  static_cast<int>(e));
-    return ZERO_EHIP;
-}
+using zs::fail_hip;
 
 constexpr int kMaxDevices = 64;
 // Per-device cache of the properties the launchers use; a zero compute-unit
@@ -175,6 +171,12 @@ int step_args(void *w16, const void *g, uintptr_t g_align, float *master, float 
 }
 
 }  // namespace
+
+int zs::fail_hip(hipError_t e, const char *what) {
+    std::snprintf(g_err, sizeof g_err, "HIP error in %s: %s (%d)", what, hipGetErrorString(e),
+                  static_cast<int>(e));
+    return ZERO_EHIP;
+}
 
 uint64_t zs::max_blocks() { return t_grid_cap; }
 

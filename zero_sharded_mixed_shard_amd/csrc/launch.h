@@ -46,6 +46,9 @@ inline bool scale_is_pow2(float S) {
     return (b & 0x807fffffu) == 0 && e >= 1 && e <= 253;
 }
 
+// ZERO_EHIP, with the text zero_strerror gives for it on this thread.
+int fail_hip(hipError_t e, const char *what);
+
 // Largest grid of the streaming kernels, in 256-thread blocks: one tile per
 // block measured fastest, and 2^23 blocks keep the grid below 2^32 threads.
 // Larger shards loop over tiles.

@@ -1,0 +1,366 @@
+// gfx950 kernels of the weight gradient G[o, i] = sum over t of dy[t, o] v[t, i],
+// v the values of an 8-bit activation checkpoint.
+//
+// The reduction runs over the tokens, the slow axis of both operands, while an
+// MFMA lane wants eight consecutive reduction steps of one row.  Both tiles are
+// staged in LDS as they lie in memory ([token][column]) and read with the
+// transposing LDS read (four tokens of one column a lane and instruction).
+// Codes become 16-bit floats on their way into LDS, where a row's exponent is the
+// same for eight neighbours: one convert makes two exact values (code * 2^k has
+// four significant bits), so products are exact and only the FP32 sum rounds.
+//
+// LDS columns are permuted in units of 16 (32 B): unit u of token t sits at
+// u ^ 2 (t mod 4), so the four token rows that 16 lanes read at once, and the
+// next 16 lanes' rows, fall on different banks.
+//
+// The loop keeps one step of global loads in registers and two steps in LDS:
+// step s multiplies buffer s mod 2 while step s+1 is written to the other and
+// step s+2 is on its way from memory, with one barrier a step.
+//
+// Few tiles: the tokens are split over `splits` blocks of a tile, which write
+// FP32 partial products; a second kernel adds them in split order.
+#include "grad_device.h"
+
+#pragma clang fp contract(off)
+
+namespace zs {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr uint32_t kStep = 64;   // tokens a step of the loop
+
+template <int F>
+__device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
+    if constexpr (F == 0)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Eight codes of one block (exponent byte eb) as eight 16-bit floats.
+template <int F>
+__device__ __forceinline__ u32x4 codes_to_16(u32x2 c, uint32_t eb) {
+    const float s = from_bits(eb << 23);
+    u32x4 r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (F == 0) {
+            r[2 * h] = __builtin_bit_cast(uint32_t,
+                                          __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[h], s, false));
+            r[2 * h + 1] = __builtin_bit_cast(
+                uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[h], s, true));
+        } else {
+            r[2 * h] = __builtin_bit_cast(
+                uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h], s, false));
+            r[2 * h + 1] = __builtin_bit_cast(
+                uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[h], s, true));
+        }
+    }
+    return r;
+}
+
+// Four tokens of one column: lanes 4r .. 4r+3 of each 16 address row r's 16 columns.
+__device__ __forceinline__ s16x4 read_tr(const uint16_t *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4 *)(p));
+}
+
+enum class Out { k16, k32, kAdd32 };   // 16-bit result, FP32 result, added to FP32
+
+struct GradShape {
+    uint64_t lddy;
+    uint32_t tokens, n_out, n_in, blocks_in;   // blocks_in: exponent bytes a row
+    uint32_t per_split;                        // tokens a split (a multiple of kStep)
+    uint32_t tiles_in;                         // tiles along n_in
+    uint64_t tiles;
+};
+
+// One BM x BN tile of G over one split of the tokens; WM x WN waves.
+template <int F, Out O, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void weight_grad_kernel(
+    void *__restrict__ out, const uint16_t *__restrict__ dy, const uint8_t *__restrict__ q,
+    const uint8_t *__restrict__ e, GradShape g) {
+    constexpr int kThreads = 64 * WM * WN;
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;     // 32x32 results a wave
+    constexpr int kRowsA = kThreads * 8 / BM, kRowsB = kThreads * 8 / BN;  // rows a pass
+    constexpr int PA = kStep / kRowsA, PB = kStep / kRowsB;                // passes a step
+    __shared__ __align__(16) uint16_t sa[2][kStep * BM];
+    __shared__ __align__(16) uint16_t sb[2][kStep * BN];
+
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    for (uint64_t tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
+    const uint32_t tile_o = static_cast<uint32_t>(tile / g.tiles_in);
+    const uint32_t o0 = tile_o * BM, i0 = static_cast<uint32_t>(tile - static_cast<uint64_t>(tile_o) * g.tiles_in) * BN;
+    const uint64_t t_first = static_cast<uint64_t>(blockIdx.y) * g.per_split;
+    const uint32_t t_begin = static_cast<uint32_t>(t_first < g.tokens ? t_first : g.tokens);
+    const uint32_t t_end = static_cast<uint32_t>(
+        t_first + g.per_split < g.tokens ? t_first + g.per_split : g.tokens);
+    const uint32_t steps = (t_end - t_begin + kStep - 1) / kStep;
+
+    // staging: this thread's eight columns and first row of each tile
+    const uint32_t ca = threadIdx.x % (BM / 8) * 8, ra = threadIdx.x / (BM / 8);
+    const uint32_t cb = threadIdx.x % (BN / 8) * 8, rb = threadIdx.x / (BN / 8);
+    const uint32_t na = o0 + ca >= g.n_out ? 0u : g.n_out - o0 - ca < 8 ? g.n_out - o0 - ca : 8u;
+    const uint32_t nb = i0 + cb >= g.n_in ? 0u : g.n_in - i0 - cb < 8 ? g.n_in - i0 - cb : 8u;
+    u32x4 xa[PA];
+    u32x2 xb[PB];
+    uint32_t eb[PB];
+    auto load = [&](uint32_t t0) {
+#pragma unroll
+        for (int p = 0; p < PA; ++p) {
+            const uint32_t t = t0 + ra + p * kRowsA;
+            xa[p] = u32x4{0u, 0u, 0u, 0u};
+            if (t < t_end) {
+                const uint16_t *s = dy + static_cast<uint64_t>(t) * g.lddy + o0 + ca;
+                if (na == 8) {
+                    xa[p] = *reinterpret_cast<const u32x4_any *>(s);
+                } else {
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j)
+                        if (j < na) xa[p][j / 2] |= static_cast<uint32_t>(s[j]) << (16 * (j % 2));
+                }
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+            const uint32_t t = t0 + rb + p * kRowsB;
+            xb[p] = u32x2{0u, 0u};
+            eb[p] = 127u;
+            if (t < t_end && nb != 0) {
+                const uint8_t *s = q + static_cast<uint64_t>(t) * g.n_in + i0 + cb;
+                eb[p] = e[static_cast<uint64_t>(t) * g.blocks_in + (i0 + cb) / ZERO_ACT_BLOCK];
+                if (nb == 8) {
+                    xb[p] = *reinterpret_cast<const u32x2_any *>(s);
+                } else {
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j)
+                        if (j < nb) xb[p][j / 4] |= static_cast<uint32_t>(s[j]) << (8 * (j % 4));
+                }
+            }
+        }
+    };
+    // LDS place of eight columns c of row r in a tile of `width` columns
+    auto place = [](uint32_t r, uint32_t c, uint32_t width) {
+        return r * width + (((c >> 4) ^ ((r & 3u) << 1)) << 4) + (c & 15u);
+    };
+    auto stage = [&](uint32_t buf) {
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+            *reinterpret_cast<u32x4 *>(&sa[buf][place(ra + p * kRowsA, ca, BM)]) = xa[p];
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+            *reinterpret_cast<u32x4 *>(&sb[buf][place(rb + p * kRowsB, cb, BN)]) =
+                codes_to_16<F>(xb[p], eb[p]);
+    };
+
+    // reading: lane (half, group of 16, j) reads row 8 half + j/4 (+4), columns
+    // 16 group + 4 (j mod 4) of a 32-column unit
+    const uint32_t half = lane >> 5, grp = (lane >> 4) & 1u, j = lane & 15u;
+    const uint32_t am = wave % WM * (BM / WM), bn = wave / WM * (BN / WN);
+    uint32_t pa[TM], pb[TN];
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+        pa[m] = place(half * 8 + (j >> 2), am + m * 32 + grp * 16 + (j & 3u) * 4, BM);
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+        pb[n] = place(half * 8 + (j >> 2), bn + n * 32 + grp * 16 + (j & 3u) * 4, BN);
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.0f;
+
+    if (steps > 0) {
+        load(t_begin);
+        stage(0);
+        if (steps > 1) load(t_begin + kStep);
+        __syncthreads();
+    }
+    for (uint32_t s = 0; s < steps; ++s) {
+        const uint32_t buf = s & 1u;
+        if (s + 1 < steps) {
+            stage(buf ^ 1u);
+            if (s + 2 < steps) load(t_begin + (s + 2) * kStep);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kStep; k += 16) {
+            s16x8 a[TM], b[TN];
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const s16x4 lo = read_tr(&sa[buf][pa[m] + k * BM]);
+                const s16x4 hi = read_tr(&sa[buf][pa[m] + (k + 4) * BM]);
+                a[m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+#pragma unroll
+            for (int n = 0; n < TN; ++n) {
+                const s16x4 lo = read_tr(&sb[buf][pb[n] + k * BN]);
+                const s16x4 hi = read_tr(&sb[buf][pb[n] + (k + 4) * BN]);
+                b[n] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+#pragma unroll
+            for (int m = 0; m < TM; ++m)
+#pragma unroll
+                for (int n = 0; n < TN; ++n) acc[m][n] = mfma<F>(a[m], b[n], acc[m][n]);
+        }
+        __syncthreads();
+    }
+
+    // result register r of a lane: row 8 (r/4) + 4 half + r%4, column lane mod 32
+    const uint64_t plane = static_cast<uint64_t>(g.n_out) * g.n_in;
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+            const uint32_t col = i0 + bn + n * 32 + (lane & 31u);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const uint32_t row = o0 + am + m * 32 + 8 * (r / 4) + 4 * half + r % 4;
+                if (row < g.n_out && col < g.n_in) {
+                    const uint64_t at = static_cast<uint64_t>(row) * g.n_in + col;
+                    if constexpr (O == Out::k16) {
+                        static_cast<uint16_t *>(out)[at] = from_f32<F>(acc[m][n][r]);
+                    } else {
+                        float *d = static_cast<float *>(out) + blockIdx.y * plane + at;
+                        *d = O == Out::kAdd32 ? *d + acc[m][n][r] : acc[m][n][r];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// dw = (dw +) the sum of `splits` planes of n FP32 values, in split order.
+constexpr int kJoinThreads = 256;
+template <int F, Out O>
+__global__ __launch_bounds__(kJoinThreads) void join_splits_kernel(
+    void *__restrict__ dw, const float *__restrict__ part, uint64_t n, uint32_t splits) {
+    const uint64_t stride = static_cast<uint64_t>(gridDim.x) * kJoinThreads;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kJoinThreads + threadIdx.x; i < n;
+         i += stride) {
+        float s = part[i];
+        for (uint32_t k = 1; k < splits; ++k) s = s + part[k * n + i];
+        if constexpr (O == Out::k16)
+            static_cast<uint16_t *>(dw)[i] = from_f32<F>(s);
+        else
+            static_cast<float *>(dw)[i] = O == Out::kAdd32 ? static_cast<float *>(dw)[i] + s : s;
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kJoinThreads) void zero_fill_kernel(T *__restrict__ d, uint64_t n) {
+    const uint64_t stride = static_cast<uint64_t>(gridDim.x) * kJoinThreads;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kJoinThreads + threadIdx.x; i < n;
+         i += stride)
+        d[i] = T(0);
+}
+
+uint32_t capped_blocks(uint64_t n) {
+    const uint64_t b = (n + kJoinThreads - 1) / kJoinThreads, cap = max_blocks();
+    return static_cast<uint32_t>(b < cap ? b : cap);
+}
+
+// Tile and splits of a call, by its extents alone (so the workspace and the order
+// of the sums do not depend on the device).
+struct Plan {
+    bool big;          // 256 x 256 tiles, else 128 x 128
+    uint32_t splits;
+    uint32_t per_split;
+};
+
+constexpr uint64_t kFill = 256;   // compute units of the chip
+
+Plan plan_of(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
+    auto tiles = [&](uint64_t b) { return ((n_out + b - 1) / b) * ((n_in + b - 1) / b); };
+    Plan p;
+    p.big = tiles(256) >= kFill;
+    const uint64_t n = tiles(p.big ? 256 : 128);
+    const uint64_t steps = (tokens + kStep - 1) / kStep;
+    uint64_t s = 1;
+    while (n * s < kFill && steps / (s + 1) >= 8) ++s;
+    const uint64_t per = (steps + s - 1) / s;
+    p.splits = static_cast<uint32_t>((steps + per - 1) / per);
+    p.per_split = static_cast<uint32_t>(per * kStep);
+    return p;
+}
+
+template <int F, Out O>
+hipError_t tiles_of(void *out, const uint16_t *dy, const uint8_t *q, const uint8_t *e,
+                    const GradShape &g, const Plan &p, hipStream_t stream) {
+    const uint64_t cap = max_blocks();
+    const dim3 grid(static_cast<uint32_t>(g.tiles < cap ? g.tiles : cap), p.splits);
+    if (p.big)
+        weight_grad_kernel<F, O, 256, 256, 4, 2><<<grid, 512, 0, stream>>>(out, dy, q, e, g);
+    else
+        weight_grad_kernel<F, O, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(out, dy, q, e, g);
+    return hipGetLastError();
+}
+
+template <int F, Out O>
+hipError_t grad_as(void *dw, const uint16_t *dy, const uint8_t *q, const uint8_t *e,
+                   const GradShape &g, const Plan &p, void *workspace, hipStream_t stream) {
+    if (p.splits == 1) return tiles_of<F, O>(dw, dy, q, e, g, p, stream);
+    const hipError_t err = tiles_of<F, Out::k32>(workspace, dy, q, e, g, p, stream);
+    if (err != hipSuccess) return err;
+    const uint64_t n = static_cast<uint64_t>(g.n_out) * g.n_in;
+    join_splits_kernel<F, O><<<capped_blocks(n), kJoinThreads, 0, stream>>>(
+        dw, static_cast<const float *>(workspace), n, p.splits);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+uint64_t weight_grad_workspace(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
+    const Plan p = plan_of(tokens, n_out, n_in);
+    return p.splits == 1 ? 0 : 4 * n_out * n_in * p.splits;
+}
+
+hipError_t launch_weight_grad(void *dw, bool dw32, bool first, const uint16_t *dy, uint64_t lddy,
+                              int fmt, const uint8_t *q, const uint8_t *e, uint64_t tokens,
+                              uint64_t n_out, uint64_t n_in, void *workspace,
+                              hipStream_t stream) {
+    const Plan p = plan_of(tokens, n_out, n_in);
+    const uint64_t b = p.big ? 256 : 128;
+    const uint64_t tiles_in = (n_in + b - 1) / b;
+    const GradShape g{lddy,
+                      static_cast<uint32_t>(tokens),
+                      static_cast<uint32_t>(n_out),
+                      static_cast<uint32_t>(n_in),
+                      static_cast<uint32_t>((n_in + ZERO_ACT_BLOCK - 1) / ZERO_ACT_BLOCK),
+                      p.per_split,
+                      static_cast<uint32_t>(tiles_in),
+                      tiles_in * ((n_out + b - 1) / b)};
+#define ZS_GRAD(F, O) return grad_as<F, O>(dw, dy, q, e, g, p, workspace, stream)
+    if (fmt == 0) {
+        if (!dw32) ZS_GRAD(0, Out::k16);
+        if (first) ZS_GRAD(0, Out::k32);
+        ZS_GRAD(0, Out::kAdd32);
+    }
+    if (!dw32) ZS_GRAD(1, Out::k16);
+    if (first) ZS_GRAD(1, Out::k32);
+    ZS_GRAD(1, Out::kAdd32);
+#undef ZS_GRAD
+}
+
+hipError_t launch_zero_fill(void *dw, int elem_bytes, uint64_t n, hipStream_t stream) {
+    if (elem_bytes == 4)
+        zero_fill_kernel<<<capped_blocks(n), kJoinThreads, 0, stream>>>(
+            static_cast<uint32_t *>(dw), n);
+    else
+        zero_fill_kernel<<<capped_blocks(n), kJoinThreads, 0, stream>>>(
+            static_cast<uint16_t *>(dw), n);
+    return hipGetLastError();
+}
+
+}  // namespace zs
