@@ -4,24 +4,24 @@
 // FP32) a lane, groups numbered over the whole output so that short and odd
 // widths fill the lanes too.
 //
-// The gradient sums the rows of dy that share an id.  Without floating-point
+// The gradient sums the rows of dy that share an id, without floating-point
 // atomics and in an order that the ids alone fix:
 //   1. the tokens are sorted by (id, position); ids outside the vocabulary sort
 //      last (key = vocab) and are never read again.
-//   2. the sorted positions are cut into chunks of C.  A chunk that lies inside
-//      one id's run is summed into a partial row (FP32 workspace), so that long
-//      runs (padding, frequent tokens) are spread over the whole chip.
-//   3. every vocabulary row finds its run by binary search, adds the positions
-//      before the first whole chunk, the whole chunks' partial rows and the
-//      positions after the last one, and writes the row (zeros for an empty run).
-// A run of R costs its wave at most 2C + R/C row loads; C is near the root of
-// T/4, where the worst case (one id everywhere) is least.
+//   2. a wave walks 64 sorted positions over 512 columns, eight rows of dy in
+//      flight.  A run of equal ids that lies inside its 64 positions is scaled,
+//      rounded and written; what reaches over an end becomes a partial row (FP32
+//      workspace).  So the work is cut evenly whatever the ids are: frequent tokens
+//      and padding spread over the whole chip.  In the same launch other blocks
+//      write the zero rows of ids that do not occur.
+//   3. the partial rows of each run that crosses chunks are added.
+// What has to move is dy once and dw once; partial rows add at most
+// 2 * 2 * 4 / (64 * 2) = 1/8 of dy.
 //
 // Sorting: up to kRankTokens tokens, a token's place is the number of keys that
-// precede it, counted directly, in one launch (T^2 compares: 2 VALU operations
-// each, measured cheaper than three dependent launches at these sizes).  More
-// tokens take a stable radix sort, kDigitBits a pass, of at most kSortBlocks
-// blocks.
+// precede it, counted directly in one launch (T^2 compares of two VALU operations
+// each).  More tokens take a stable radix sort, kDigitBits a pass, two launches a
+// pass.
 #include "grad_device.h"
 
 #pragma clang fp contract(off)
@@ -143,10 +143,10 @@ __global__ __launch_bounds__(kRankThreads) void rank_sort_kernel(
 
 constexpr int kDigitBits = 9;
 constexpr uint32_t kDigits = 1u << kDigitBits;
-constexpr uint32_t kSortBlocks = 64;
+constexpr uint32_t kSortBlocks = 128;
 constexpr int kSortThreads = 256;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr uint32_t kSortMin = 4096;           // tokens a sort block takes at least
+constexpr uint32_t kSortMin = 1024;           // tokens a sort block takes at least
 
 // Lanes of the wave whose digit equals this lane's, among the active ones.
 __device__ __forceinline__ uint64_t peers_of(uint32_t digit, bool on) {
@@ -166,27 +166,16 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // Digit counts of each wave's share of a block's tokens, in LDS; the shares are
-// consecutive, so (wave, step, lane) is the token order.  per_wave is a multiple of 64.
+// consecutive, so (wave, step, lane) is the token order.
 template <typename Load>
 __device__ __forceinline__ void wave_histogram(uint32_t (*cnt)[kDigits], uint32_t first,
                                                uint32_t last, int shift, Load key_of) {
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     for (uint32_t d = lane; d < kDigits; d += 64) cnt[wave][d] = 0;
     wave_sync();
-    for (uint32_t t0 = first; t0 < last; t0 += 64) {
-        const uint32_t t = t0 + lane;
-        const bool on = t < last;
-        const uint32_t digit = on ? (key_of(t) >> shift) & (kDigits - 1) : 0u;
-        const uint64_t m = peers_of(digit, on);
-        if (on && (m & ((1ull << lane) - 1)) == 0)
-            cnt[wave][digit] += static_cast<uint32_t>(__popcll(m));
-        wave_sync();
-    }
+    for (uint32_t t = first + lane; t < last; t += 64)
+        atomicAdd(&cnt[wave][(key_of(t) >> shift) & (kDigits - 1)], 1u);
 }
-
-struct SortShape {
-    uint32_t blocks, per_block;   // per_block: a multiple of 256
-};
 
 // The first pass reads ids (keys_in null); later passes read keys and order.
 __global__ __launch_bounds__(kSortThreads) void radix_count_kernel(
@@ -207,7 +196,7 @@ __global__ __launch_bounds__(kSortThreads) void radix_count_kernel(
         uint32_t s = 0;
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) s += cnt[w][d];
-        hist[d * kSortBlocks + blockIdx.x] = s;
+        hist[blockIdx.x * kDigits + d] = s;
     }
 }
 
@@ -229,19 +218,19 @@ __global__ __launch_bounds__(kSortThreads) void radix_scatter_kernel(
     };
     wave_histogram(cnt, first, last, shift, key_of);
     // a digit's tokens over all blocks, and over the blocks before this one
-    uint32_t before[kDigits / kSortThreads];
+    constexpr uint32_t kMine = kDigits / kSortThreads;
+    uint32_t before[kMine] = {}, all[kMine] = {};
+#pragma unroll 8
+    for (uint32_t b = 0; b < gridDim.x; ++b) {
 #pragma unroll
-    for (uint32_t i = 0; i < kDigits / kSortThreads; ++i) {
-        const uint32_t d = threadIdx.x + i * kSortThreads;
-        uint32_t all = 0, bef = 0;
-        for (uint32_t b = 0; b < gridDim.x; ++b) {
-            const uint32_t h = hist[d * kSortBlocks + b];
-            all += h;
-            bef += b < blockIdx.x ? h : 0u;
+        for (uint32_t i = 0; i < kMine; ++i) {
+            const uint32_t h = hist[b * kDigits + threadIdx.x + i * kSortThreads];
+            all[i] += h;
+            before[i] += b < blockIdx.x ? h : 0u;
         }
-        total[d] = all;
-        before[i] = bef;
     }
+#pragma unroll
+    for (uint32_t i = 0; i < kMine; ++i) total[threadIdx.x + i * kSortThreads] = all[i];
     __syncthreads();
     // exclusive scan of total over the digits, by wave 0: eight digits a lane
     if (wave == 0) {
@@ -300,164 +289,252 @@ __global__ __launch_bounds__(kSortThreads) void radix_scatter_kernel(
 
 // ---- summing the rows --------------------------------------------------------------
 
-constexpr int kRowThreads = 256;
-constexpr int kRowWaves = kRowThreads / 64;
-constexpr uint32_t kRowsPerBlock = 16;    // vocabulary rows a block searches for at once
+constexpr int kSumThreads = 256;
+constexpr int kSumWaves = kSumThreads / 64;
 constexpr uint32_t kSlice = 512;          // columns a wave covers (8 a lane)
+constexpr uint32_t kChunk = 64;           // sorted positions a wave walks: one a lane
+constexpr uint32_t kZeroRows = 32;        // vocabulary rows a zeroing block looks at
+constexpr int kJoinThreads = 512;
+constexpr int kJoinWaves = kJoinThreads / 64;
 
-// acc[0..8) += the eight columns at col of dy's rows order[lo .. hi), in that
-// order; four rows' loads in flight.
-template <int F>
-__device__ __forceinline__ void add_rows(float acc[8], const uint16_t *__restrict__ dy,
-                                         uint64_t lddy, const uint32_t *__restrict__ order,
-                                         uint32_t lo, uint32_t hi, uint32_t col, uint32_t n) {
-    constexpr uint32_t U = 4;
-    if (n == 8) {
-        uint32_t p = lo;
-        for (; p + U <= hi; p += U) {
-            Raw8<F> r[U];
+// What the summing kernels share.
+struct RowSums {
+    const uint16_t *dy;
+    uint64_t lddy;
+    const uint32_t *keys, *order;   // sorted tokens
+    float *part;                    // partial rows: two a chunk, ld_part columns each
+    uint32_t ld_part, tokens, vocab, width;
+    uint32_t chunks, slices;
+    float scale;
+};
+
+// Eight columns of a finished row: scaled, added to the old row (not FIRST), rounded.
+template <int O, bool FIRST>
+__device__ __forceinline__ void finish_row(elem_t<O> *dw, const RowSums &a, uint32_t key,
+                                           uint32_t col, uint32_t n, const float acc[8]) {
+    elem_t<O> *d = dw + static_cast<uint64_t>(key) * a.width + col;
+    float v[8];
 #pragma unroll
-            for (uint32_t u = 0; u < U; ++u)
-                r[u] = load8<F>(dy + static_cast<uint64_t>(order[p + u]) * lddy + col);
+    for (int j = 0; j < 8; ++j) v[j] = product32(acc[j], a.scale);
+    if constexpr (!FIRST) {
+        float old[8];
+        if (n == 8)
+            widen8<O>(load8<O>(d), old);
+        else
+            load_some<O>(d, n, old);
 #pragma unroll
-            for (uint32_t u = 0; u < U; ++u) {
-                float x[8];
-                widen8<F>(r[u], x);
+        for (int j = 0; j < 8; ++j) v[j] = old[j] + v[j];
+    }
+    if (n == 8)
+        store8<O>(d, v);
+    else
+        store_some<O>(d, n, v);
+}
+
+__device__ __forceinline__ float *part_row(const RowSums &a, uint64_t chunk, uint32_t slot,
+                                           uint32_t col) {
+    return a.part + (chunk * 2 + slot) * a.ld_part + col;
+}
+
+__device__ __forceinline__ void store_part(float *p, const float v[8]) {
+    f32x4 *d = reinterpret_cast<f32x4 *>(p);
+    d[0] = f32x4{v[0], v[1], v[2], v[3]};
+    d[1] = f32x4{v[4], v[5], v[6], v[7]};
+}
+
+// One wave: the columns [col, col + n) a lane of chunk c's positions.  A run inside
+// the chunk is finished here; a run that came from the chunk before (or fills the
+// whole chunk) goes to slot 0, one that starts here and goes on to slot 1.
+template <int F, int O, bool FIRST>
+__device__ __forceinline__ void sum_chunk(elem_t<O> *dw, const RowSums &a, uint32_t c,
+                                          uint32_t col, uint32_t n) {
+    constexpr int U = 8;              // rows in flight
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t lo = c * kChunk, p = lo + lane;
+    const uint32_t key = p < a.tokens ? a.keys[p] : a.vocab;
+    const uint32_t row = p < a.tokens ? a.order[p] : 0u;
+    const uint32_t count = static_cast<uint32_t>(__popcll(__ballot(key < a.vocab)));
+    if (count == 0) return;           // ids outside the vocabulary sort last
+    const uint32_t next = lo + kChunk < a.tokens ? a.keys[lo + kChunk] : a.vocab;
+    const uint32_t prev = lo > 0 ? a.keys[lo - 1] : a.vocab;
+    uint32_t after = __shfl_down(key, 1);
+    if (lane == 63) after = next;
+    const uint64_t ends = __ballot(after != key);   // last positions of their runs
+    bool from_before = __builtin_amdgcn_readfirstlane(key) == prev;
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (uint32_t i0 = 0; i0 < count; i0 += U) {
+        Raw8<F> r[U];
+        float x[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] += x[j];
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = i0 + u < count ? i0 + u : count - 1;
+            const uint64_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(row, i));
+            const uint16_t *s = a.dy + t * a.lddy + col;
+            if (n == 8) {
+                r[u] = load8<F>(s);
+            } else if (n != 0) {
+                r[u].v[0] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    if (j < n) r[u].v[0][j / 2] |= static_cast<uint32_t>(s[j]) << (16 * (j % 2));
             }
         }
-        for (; p < hi; ++p) {
-            float x[8];
-            widen8<F>(load8<F>(dy + static_cast<uint64_t>(order[p]) * lddy + col), x);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = i0 + u;
+            if (i >= count) break;
+            widen8<F>(r[u], x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] += x[j];
-        }
-    } else {
-        for (uint32_t p = lo; p < hi; ++p) {
-            float x[8];
-            load_some<F>(dy + static_cast<uint64_t>(order[p]) * lddy + col, n, x);
+            const bool end = (ends >> i) & 1u;
+            if (end || i == kChunk - 1) {
+                if (n != 0) {
+                    if (from_before)
+                        store_part(part_row(a, c, 0, col), acc);
+                    else if (!end)
+                        store_part(part_row(a, c, 1, col), acc);
+                    else
+                        finish_row<O, FIRST>(
+                            dw, a, static_cast<uint32_t>(__builtin_amdgcn_readlane(key, i)), col,
+                            n, acc);
+                }
+                from_before = false;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += x[j];
+                for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+            }
         }
     }
 }
 
-// Partial rows of the chunks that lie inside one run.  blockIdx.x: chunk;
-// blockIdx.y and the wave: slice of columns.  part holds ld_part (a multiple of
-// 8) FP32 columns a chunk.
-template <int F>
-__global__ __launch_bounds__(kRowThreads) void chunk_sum_kernel(
-    float *__restrict__ part, uint32_t ld_part, const uint16_t *__restrict__ dy, uint64_t lddy,
-    const uint32_t *__restrict__ keys, const uint32_t *__restrict__ order, uint32_t vocab,
-    uint32_t width, uint32_t chunk) {
-    const uint32_t lo = blockIdx.x * chunk, hi = lo + chunk;   // whole chunks only
-    const uint32_t key = keys[lo];
-    if (key >= vocab || keys[hi - 1] != key) return;
-    const uint32_t slices = (width + kSlice - 1) / kSlice;
-    for (uint32_t s = blockIdx.y * kRowWaves + (threadIdx.x >> 6); s < slices;
-         s += gridDim.y * kRowWaves) {
-        const uint32_t col = s * kSlice + (threadIdx.x & 63u) * 8;
-        if (col >= width) return;
-        const uint32_t n = width - col < 8 ? width - col : 8;
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        add_rows<F>(acc, dy, lddy, order, lo, hi, col, n);
-        f32x4 *d =
-            reinterpret_cast<f32x4 *>(part + static_cast<uint64_t>(blockIdx.x) * ld_part + col);
-        d[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
-        d[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+// First sorted position whose key is at least want.
+__device__ __forceinline__ uint32_t lower_bound(const uint32_t *keys, uint32_t tokens,
+                                                uint32_t want) {
+    uint32_t lo = 0, hi = tokens;
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        if (keys[mid] < want)
+            lo = mid + 1;
+        else
+            hi = mid;
     }
+    return lo;
 }
 
-// The vocabulary rows.  O: dw's format.  FIRST false (FP32 only): rows whose id
-// occurs get dw + G, the others are left alone.
-template <int F, int O, bool FIRST>
-__global__ __launch_bounds__(kRowThreads) void row_sum_kernel(
-    elem_t<O> *__restrict__ dw, const uint16_t *__restrict__ dy, uint64_t lddy,
-    const uint32_t *__restrict__ keys, const uint32_t *__restrict__ order,
-    const float *__restrict__ part, uint32_t ld_part, uint32_t tokens, uint32_t vocab,
-    uint32_t width, uint32_t chunk, int chunk_shift, float scale) {
-    __shared__ uint32_t start[kRowsPerBlock + 1];
-    for (uint32_t v0 = blockIdx.x * kRowsPerBlock; v0 < vocab; v0 += gridDim.x * kRowsPerBlock) {
-    const uint32_t rows = vocab - v0 < kRowsPerBlock ? vocab - v0 : kRowsPerBlock;
-    if (threadIdx.x <= rows) {      // first sorted position whose key is >= v0 + lane
-        const uint32_t want = v0 + threadIdx.x;
-        uint32_t lo = 0, hi = tokens;
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            if (keys[mid] < want)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        start[threadIdx.x] = lo;
+// Zeros in the rows of a group of kZeroRows whose id does not occur.
+template <int O>
+__device__ __forceinline__ void zero_rows(elem_t<O> *dw, const RowSums &a, uint32_t group,
+                                          const FastDiv &per_row) {
+    __shared__ uint32_t start[kZeroRows + 1];
+    const uint32_t v0 = group * kZeroRows;
+    const uint32_t rows = a.vocab - v0 < kZeroRows ? a.vocab - v0 : kZeroRows;
+    if (threadIdx.x <= rows) start[threadIdx.x] = lower_bound(a.keys, a.tokens, v0 + threadIdx.x);
+    __syncthreads();
+    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const uint64_t items = static_cast<uint64_t>(rows) * per_row.d;
+    for (uint64_t i = threadIdx.x; i < items; i += kSumThreads) {
+        const uint32_t r = static_cast<uint32_t>(div_by(i, per_row));
+        if (start[r] != start[r + 1]) continue;
+        const uint32_t col = static_cast<uint32_t>(i - static_cast<uint64_t>(r) * per_row.d) * 8;
+        elem_t<O> *d = dw + static_cast<uint64_t>(v0 + r) * a.width + col;
+        if (a.width - col >= 8)
+            store8<O>(d, zero);
+        else
+            store_some<O>(d, a.width - col, zero);
     }
     __syncthreads();
-    const uint32_t slices = (width + kSlice - 1) / kSlice;
+}
+
+// The chunks' sums, and with FIRST the zero rows, in one launch: the sums read and
+// the zeros write, so they share the memory's time.  Work items: `sum_blocks` groups
+// of kSumWaves (chunk, slice) pairs, then `zero_blocks` groups of rows.
+template <int F, int O, bool FIRST>
+__global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(
+    elem_t<O> *__restrict__ dw, RowSums a, FastDiv slices, FastDiv per_row, uint64_t sum_blocks,
+    uint64_t zero_blocks) {
+    for (uint64_t b = blockIdx.x; b < sum_blocks + zero_blocks; b += gridDim.x) {
+        if (b < sum_blocks) {
+            const uint64_t w = b * kSumWaves + (threadIdx.x >> 6);
+            const uint64_t c = div_by(w, slices);
+            if (c >= a.chunks) continue;
+            const uint64_t col =
+                (w - c * slices.d) * kSlice + static_cast<uint64_t>(threadIdx.x & 63u) * 8;
+            const uint32_t n = col >= a.width ? 0u
+                               : a.width - col < 8 ? static_cast<uint32_t>(a.width - col) : 8u;
+            sum_chunk<F, O, FIRST>(dw, a, __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(c)),
+                                   static_cast<uint32_t>(col), n);
+        } else {
+            if constexpr (FIRST)
+                zero_rows<O>(dw, a, static_cast<uint32_t>(b - sum_blocks), per_row);
+        }
+    }
+}
+
+// Runs that cross chunks: the block of the chunk where such a run starts adds its
+// partial rows (slot 1 of that chunk, slot 0 of the following ones), each wave a
+// consecutive share of them, then the waves' sums in order.  blockIdx.y: slices.
+template <int O, bool FIRST>
+__global__ __launch_bounds__(kJoinThreads) void join_runs_kernel(elem_t<O> *__restrict__ dw,
+                                                                 RowSums a) {
+    __shared__ float sums[kJoinWaves][kSlice];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
-    for (uint32_t w = wave; w < rows * slices; w += kRowWaves) {
-        const uint32_t r = w / slices, col = (w - r * slices) * kSlice + lane * 8;
-        if (col >= width) continue;
-        const uint32_t n = width - col < 8 ? width - col : 8;
-        const uint32_t lo = start[r], hi = start[r + 1];
-        if (!FIRST && lo == hi) continue;
+    const uint32_t c = blockIdx.x, hi = (c + 1) * kChunk;
+    if (hi >= a.tokens) return;
+    const uint32_t key = a.keys[hi - 1];
+    if (key >= a.vocab || a.keys[hi] != key) return;                    // nothing goes on
+    const uint32_t lo = c * kChunk;
+    if (a.keys[lo] == key && lo > 0 && a.keys[lo - 1] == key) return;   // it started before
+    const uint32_t last = lower_bound(a.keys, a.tokens, key + 1) - 1;   // of the run
+    const uint32_t n_part = last / kChunk - c + 1;
+    const uint32_t p0 = static_cast<uint32_t>(static_cast<uint64_t>(n_part) * wave / kJoinWaves);
+    const uint32_t p1 =
+        static_cast<uint32_t>(static_cast<uint64_t>(n_part) * (wave + 1) / kJoinWaves);
+    for (uint32_t s = blockIdx.y; s < a.slices; s += gridDim.y) {
+        const uint32_t col = s * kSlice + lane * 8;
         float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        const uint32_t c0 = (lo + chunk - 1) >> chunk_shift, c1 = hi >> chunk_shift;
-        if (c0 < c1) {
-            add_rows<F>(acc, dy, lddy, order, lo, c0 << chunk_shift, col, n);
-            for (uint32_t c = c0; c < c1; ++c) {
-                const f32x4 *s = reinterpret_cast<const f32x4 *>(
-                    part + static_cast<uint64_t>(c) * ld_part + col);
-                const f32x4 a = s[0], b = s[1];
+        if (col < a.width) {
+            constexpr uint32_t U = 4;
+            for (uint32_t p = p0; p < p1; p += U) {
+                f32x4 x[U][2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[j] += a[j];
-                    acc[4 + j] += b[j];
+                for (uint32_t u = 0; u < U; ++u) {
+                    const uint32_t i = p + u < p1 ? p + u : p1 - 1;
+                    const f32x4 *v = reinterpret_cast<const f32x4 *>(
+                        part_row(a, static_cast<uint64_t>(c) + i, i == 0 ? 1 : 0, col));
+                    x[u][0] = v[0];
+                    x[u][1] = v[1];
+                }
+#pragma unroll
+                for (uint32_t u = 0; u < U; ++u) {
+                    if (p + u >= p1) break;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[j] += x[u][j / 4][j % 4];
                 }
             }
-            add_rows<F>(acc, dy, lddy, order, c1 << chunk_shift, hi, col, n);
-        } else {
-            add_rows<F>(acc, dy, lddy, order, lo, hi, col, n);
         }
+        f32x4 *d = reinterpret_cast<f32x4 *>(&sums[wave][lane * 8]);
+        d[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
+        d[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+        __syncthreads();
+        if (wave == 0 && col < a.width) {
+            for (int w = 1; w < kJoinWaves; ++w)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = product32(acc[j], scale);
-        elem_t<O> *d = dw + static_cast<uint64_t>(v0 + r) * width + col;
-        if constexpr (!FIRST) {
-            float old[8];
-            if (n == 8)
-                widen8<O>(load8<O>(d), old);
-            else
-                load_some<O>(d, n, old);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = old[j] + acc[j];
+                for (int j = 0; j < 8; ++j) acc[j] += sums[w][lane * 8 + j];
+            finish_row<O, FIRST>(dw, a, key, col, a.width - col < 8 ? a.width - col : 8, acc);
         }
-        if (n == 8)
-            store8<O>(d, acc);
-        else
-            store_some<O>(d, n, acc);
+        __syncthreads();
     }
-    __syncthreads();   // start is rewritten
-    }
-}
-
-// Sorted positions a chunk holds: the power of two near sqrt(T) / 2, at least 32.
-int chunk_shift_of(uint64_t tokens) {
-    int s = 5;
-    while ((1ull << (2 * s)) < tokens / 4) ++s;
-    return s;
-}
-
-SortShape sort_shape(uint64_t tokens) {
-    uint64_t per = (tokens + kSortBlocks - 1) / kSortBlocks;
-    if (per < kSortMin) per = kSortMin;
-    per = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
-    return SortShape{static_cast<uint32_t>((tokens + per - 1) / per), static_cast<uint32_t>(per)};
 }
 
 uint64_t round256(uint64_t b) { return (b + 255) / 256 * 256; }
 
+uint32_t sort_per_block(uint64_t tokens) {
+    uint64_t per = (tokens + kSortBlocks - 1) / kSortBlocks;
+    if (per < kSortMin) per = kSortMin;
+    return static_cast<uint32_t>((per + kSortThreads - 1) / kSortThreads * kSortThreads);
+}
+
 // Workspace: sorted keys and order; for the radix sort a second pair and the
-// digit counts; the chunks' partial rows.
+// digit counts; the chunks' partial rows (when there are two chunks).
 struct GradSpace {
     uint64_t keys, order, keys2, order2, hist, part, total, ld_part;
     bool rank;
@@ -477,32 +554,25 @@ GradSpace grad_space(uint64_t tokens, uint64_t width) {
     }
     s.ld_part = (width + 7) / 8 * 8;
     s.part = at;
-    s.total = at + 4 * s.ld_part * (tokens >> chunk_shift_of(tokens));
+    const uint64_t chunks = (tokens + kChunk - 1) / kChunk;
+    s.total = at + (chunks > 1 ? 8 * s.ld_part * chunks : 0);
     return s;
 }
 
 template <int F, int O, bool FIRST>
-hipError_t sum_rows(void *dw, const uint16_t *dy, uint64_t lddy, const uint32_t *keys,
-                    const uint32_t *order, float *part, uint32_t ld_part, uint64_t tokens,
-                    uint64_t vocab, uint64_t width, float scale, hipStream_t stream) {
-    const int shift = chunk_shift_of(tokens);
-    const uint32_t chunks = static_cast<uint32_t>(tokens >> shift);
-    if (chunks > 0) {
-        const uint32_t per = kSlice * kRowWaves;
-        const uint64_t slices = (width + per - 1) / per;
-        const dim3 grid(chunks, static_cast<uint32_t>(slices < 65535 ? slices : 65535));
-        chunk_sum_kernel<F><<<grid, kRowThreads, 0, stream>>>(
-            part, ld_part, dy, lddy, keys, order, static_cast<uint32_t>(vocab),
-            static_cast<uint32_t>(width), 1u << shift);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    const uint64_t groups = (vocab + kRowsPerBlock - 1) / kRowsPerBlock, cap = max_blocks();
-    const uint32_t blocks = static_cast<uint32_t>(groups < cap ? groups : cap);
-    row_sum_kernel<F, O, FIRST><<<blocks, kRowThreads, 0, stream>>>(
-        static_cast<elem_t<O> *>(dw), dy, lddy, keys, order, part, ld_part,
-        static_cast<uint32_t>(tokens), static_cast<uint32_t>(vocab),
-        static_cast<uint32_t>(width), 1u << shift, shift, scale);
+hipError_t sum_rows(void *dw, const RowSums &a, hipStream_t stream) {
+    auto *d = static_cast<elem_t<O> *>(dw);
+    const uint64_t cap = max_blocks();
+    const uint64_t sums =
+        (static_cast<uint64_t>(a.chunks) * a.slices + kSumWaves - 1) / kSumWaves;
+    const uint64_t zeros = FIRST ? (static_cast<uint64_t>(a.vocab) + kZeroRows - 1) / kZeroRows : 0;
+    const uint64_t blocks = sums + zeros < cap ? sums + zeros : cap;
+    chunk_sum_kernel<F, O, FIRST><<<static_cast<uint32_t>(blocks), kSumThreads, 0, stream>>>(
+        d, a, fast_div(a.slices), fast_div((a.width + 7) / 8), sums, zeros);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.chunks < 2) return e;
+    const dim3 grid(a.chunks - 1, a.slices < 65535 ? a.slices : 65535);
+    join_runs_kernel<O, FIRST><<<grid, kJoinThreads, 0, stream>>>(d, a);
     return hipGetLastError();
 }
 
@@ -550,17 +620,18 @@ hipError_t launch_embed_grad(void *dw, bool dw32, bool first, const uint16_t *dy
         int key_bits = 1;                        // keys are 0 .. vocab
         while ((vocab >> key_bits) != 0) ++key_bits;
         const int passes = (key_bits + kDigitBits - 1) / kDigitBits;
-        const SortShape sh = sort_shape(tokens);
+        const uint32_t per = sort_per_block(tokens);
+        const uint32_t blocks = static_cast<uint32_t>((tokens + per - 1) / per);
         uint32_t *hist = list(s.hist);
         // the last pass writes the pair (keys, order)
         uint32_t *k_out = passes % 2 ? keys : list(s.keys2);
         uint32_t *o_out = passes % 2 ? order : list(s.order2);
         const uint32_t *k_in = nullptr, *o_in = nullptr;
         for (int p = 0; p < passes; ++p) {
-            radix_count_kernel<<<sh.blocks, kSortThreads, 0, stream>>>(
-                hist, k_in, ids, i64, T, V, sh.per_block, p * kDigitBits);
-            radix_scatter_kernel<<<sh.blocks, kSortThreads, 0, stream>>>(
-                k_out, o_out, hist, k_in, o_in, ids, i64, T, V, sh.per_block, p * kDigitBits);
+            radix_count_kernel<<<blocks, kSortThreads, 0, stream>>>(
+                hist, k_in, ids, i64, T, V, per, p * kDigitBits);
+            radix_scatter_kernel<<<blocks, kSortThreads, 0, stream>>>(
+                k_out, o_out, hist, k_in, o_in, ids, i64, T, V, per, p * kDigitBits);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
             k_in = k_out;
@@ -569,10 +640,11 @@ hipError_t launch_embed_grad(void *dw, bool dw32, bool first, const uint16_t *dy
             o_out = o_out == order ? list(s.order2) : order;
         }
     }
-    auto *part = reinterpret_cast<float *>(base + s.part);
-    const uint32_t ldp = static_cast<uint32_t>(s.ld_part);
-#define ZS_ROWS(F, O, FIRST) \
-    return sum_rows<F, O, FIRST>(dw, dy, lddy, keys, order, part, ldp, tokens, vocab, width, scale, stream)
+    const RowSums a{dy, lddy, keys, order, reinterpret_cast<float *>(base + s.part),
+                    static_cast<uint32_t>(s.ld_part), T, V, static_cast<uint32_t>(width),
+                    static_cast<uint32_t>((tokens + kChunk - 1) / kChunk),
+                    static_cast<uint32_t>((width + kSlice - 1) / kSlice), scale};
+#define ZS_ROWS(F, O, FIRST) return sum_rows<F, O, FIRST>(dw, a, stream)
     if (fmt == 0) {
         if (!dw32) ZS_ROWS(0, 0, true);
         if (first) ZS_ROWS(0, 2, true);
