@@ -292,10 +292,14 @@ __global__ __launch_bounds__(kSortThreads) void radix_scatter_kernel(
 constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / 64;
 constexpr uint32_t kSlice = 512;          // columns a wave covers (8 a lane)
-constexpr uint32_t kChunk = 64;           // sorted positions a wave walks: one a lane
-constexpr uint32_t kZeroRows = 32;        // vocabulary rows a zeroing block looks at
+// Sorted positions a wave walks, held one a lane: 64, or 16 where 64 would leave most
+// of the chip idle (the walk is then latency: 1024 x 768 took 16.5 us with 64).
+constexpr uint32_t kLongChunk = 64, kShortChunk = 16;
+constexpr uint64_t kFullWaves = 2048;     // two waves on each SIMD of the chip
+constexpr uint32_t kZeroRows = 64;        // vocabulary rows a zeroing block looks at: one a lane
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWaves = kJoinThreads / 64;
+constexpr uint32_t kJoinChunks = 16, kJoinColumns = 256, kShortRun = 16;
 
 // What the summing kernels share.
 struct RowSums {
@@ -345,26 +349,26 @@ __device__ __forceinline__ void store_part(float *p, const float v[8]) {
 // One wave: the columns [col, col + n) a lane of chunk c's positions.  A run inside
 // the chunk is finished here; a run that came from the chunk before (or fills the
 // whole chunk) goes to slot 0, one that starts here and goes on to slot 1.
-template <int F, int O, bool FIRST>
+template <int F, int O, bool FIRST, uint32_t kChunk>
 __device__ __forceinline__ void sum_chunk(elem_t<O> *dw, const RowSums &a, uint32_t c,
                                           uint32_t col, uint32_t n) {
     constexpr int U = 8;              // rows in flight
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t lo = c * kChunk, p = lo + lane;
-    const uint32_t key = p < a.tokens ? a.keys[p] : a.vocab;
-    const uint32_t row = p < a.tokens ? a.order[p] : 0u;
+    const bool mine = lane < kChunk && p < a.tokens;
+    const uint32_t key = mine ? a.keys[p] : a.vocab;
+    const uint32_t row = mine ? a.order[p] : 0u;
     const uint32_t count = static_cast<uint32_t>(__popcll(__ballot(key < a.vocab)));
     if (count == 0) return;           // ids outside the vocabulary sort last
     const uint32_t next = lo + kChunk < a.tokens ? a.keys[lo + kChunk] : a.vocab;
     const uint32_t prev = lo > 0 ? a.keys[lo - 1] : a.vocab;
     uint32_t after = __shfl_down(key, 1);
-    if (lane == 63) after = next;
+    if (lane == kChunk - 1) after = next;
     const uint64_t ends = __ballot(after != key);   // last positions of their runs
     bool from_before = __builtin_amdgcn_readfirstlane(key) == prev;
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (uint32_t i0 = 0; i0 < count; i0 += U) {
         Raw8<F> r[U];
-        float x[8];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t i = i0 + u < count ? i0 + u : count - 1;
@@ -383,6 +387,7 @@ __device__ __forceinline__ void sum_chunk(elem_t<O> *dw, const RowSums &a, uint3
         for (int u = 0; u < U; ++u) {
             const uint32_t i = i0 + u;
             if (i >= count) break;
+            float x[8];
             widen8<F>(r[u], x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] += x[j];
@@ -406,40 +411,63 @@ __device__ __forceinline__ void sum_chunk(elem_t<O> *dw, const RowSums &a, uint3
     }
 }
 
-// First sorted position whose key is at least want.
-__device__ __forceinline__ uint32_t lower_bound(const uint32_t *keys, uint32_t tokens,
-                                                uint32_t want) {
-    uint32_t lo = 0, hi = tokens;
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (keys[mid] < want)
-            lo = mid + 1;
-        else
-            hi = mid;
+// First sorted position whose key is at least want, by a whole wave: 64 probes a step.
+__device__ __forceinline__ uint32_t wave_lower_bound(const uint32_t *keys, uint32_t tokens,
+                                                     uint32_t want) {
+    const uint32_t lane = threadIdx.x & 63u;
+    uint32_t lo = 0, len = tokens;   // the answer is in [lo, lo + len]
+    while (len > 0) {
+        const uint32_t step = (len + 63) / 64;
+        const uint64_t at = static_cast<uint64_t>(lane) * step + step - 1;
+        const bool less = at < len && keys[lo + at] < want;
+        const uint32_t n = static_cast<uint32_t>(__popcll(__ballot(less)));
+        lo += n * step;
+        len -= n * step;
+        if (len > step - 1) len = step - 1;   // probe n is not below want
     }
     return lo;
 }
 
+// 16-B aligned zeros over [d, d + n) by the whole block, element by element at the ends.
+template <typename T>
+__device__ __forceinline__ void block_zero(T *d, uint64_t n) {
+    constexpr uint32_t K = 16 / sizeof(T);
+    const uint64_t to_line = ((16 - reinterpret_cast<uintptr_t>(d) % 16) % 16) / sizeof(T);
+    const uint64_t head = to_line < n ? to_line : n;
+    const uint64_t n_vec = (n - head) / K;
+    if (threadIdx.x < head) d[threadIdx.x] = T(0);
+    for (uint64_t i = threadIdx.x; i < n_vec; i += kSumThreads)
+        __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u},
+                                    reinterpret_cast<u32x4 *>(d + head) + i);
+    const uint64_t tail = head + n_vec * K + threadIdx.x;
+    if (tail < n) d[tail] = T(0);
+}
+
 // Zeros in the rows of a group of kZeroRows whose id does not occur.
 template <int O>
-__device__ __forceinline__ void zero_rows(elem_t<O> *dw, const RowSums &a, uint32_t group,
-                                          const FastDiv &per_row) {
-    __shared__ uint32_t start[kZeroRows + 1];
-    const uint32_t v0 = group * kZeroRows;
+__device__ __forceinline__ void zero_rows(elem_t<O> *dw, const RowSums &a, uint32_t group) {
+    __shared__ uint32_t bounds[2];
+    __shared__ uint32_t seen[kZeroRows];
+    const uint32_t v0 = group * kZeroRows, wave = threadIdx.x >> 6;
     const uint32_t rows = a.vocab - v0 < kZeroRows ? a.vocab - v0 : kZeroRows;
-    if (threadIdx.x <= rows) start[threadIdx.x] = lower_bound(a.keys, a.tokens, v0 + threadIdx.x);
+    if (threadIdx.x < kZeroRows) seen[threadIdx.x] = 0;
+    if (wave < 2) {
+        const uint32_t r = wave_lower_bound(a.keys, a.tokens, v0 + (wave == 0 ? 0 : rows));
+        if ((threadIdx.x & 63u) == 0) bounds[wave] = r;
+    }
     __syncthreads();
-    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const uint64_t items = static_cast<uint64_t>(rows) * per_row.d;
-    for (uint64_t i = threadIdx.x; i < items; i += kSumThreads) {
-        const uint32_t r = static_cast<uint32_t>(div_by(i, per_row));
-        if (start[r] != start[r + 1]) continue;
-        const uint32_t col = static_cast<uint32_t>(i - static_cast<uint64_t>(r) * per_row.d) * 8;
-        elem_t<O> *d = dw + static_cast<uint64_t>(v0 + r) * a.width + col;
-        if (a.width - col >= 8)
-            store8<O>(d, zero);
-        else
-            store_some<O>(d, a.width - col, zero);
+    for (uint32_t p = bounds[0] + threadIdx.x; p < bounds[1]; p += kSumThreads)
+        seen[a.keys[p] - v0] = 1;
+    __syncthreads();
+    const uint32_t lane = threadIdx.x & 63u;
+    uint64_t empty = __ballot(lane < rows && seen[lane] == 0);   // rows that do not occur
+    while (empty != 0) {                                         // run by run
+        const uint32_t r = static_cast<uint32_t>(__builtin_ctzll(empty));
+        const uint64_t rest = ~(empty >> r);
+        const uint32_t n = rest != 0 ? static_cast<uint32_t>(__builtin_ctzll(rest)) : 64u - r;
+        block_zero(dw + static_cast<uint64_t>(v0 + r) * a.width,
+                   static_cast<uint64_t>(n) * a.width);
+        empty = r + n < 64 ? empty >> (r + n) << (r + n) : 0;
     }
     __syncthreads();
 }
@@ -447,9 +475,9 @@ __device__ __forceinline__ void zero_rows(elem_t<O> *dw, const RowSums &a, uint3
 // The chunks' sums, and with FIRST the zero rows, in one launch: the sums read and
 // the zeros write, so they share the memory's time.  Work items: `sum_blocks` groups
 // of kSumWaves (chunk, slice) pairs, then `zero_blocks` groups of rows.
-template <int F, int O, bool FIRST>
+template <int F, int O, bool FIRST, uint32_t kChunk>
 __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(
-    elem_t<O> *__restrict__ dw, RowSums a, FastDiv slices, FastDiv per_row, uint64_t sum_blocks,
+    elem_t<O> *__restrict__ dw, RowSums a, FastDiv slices, uint64_t sum_blocks,
     uint64_t zero_blocks) {
     for (uint64_t b = blockIdx.x; b < sum_blocks + zero_blocks; b += gridDim.x) {
         if (b < sum_blocks) {
@@ -460,68 +488,111 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(
                 (w - c * slices.d) * kSlice + static_cast<uint64_t>(threadIdx.x & 63u) * 8;
             const uint32_t n = col >= a.width ? 0u
                                : a.width - col < 8 ? static_cast<uint32_t>(a.width - col) : 8u;
-            sum_chunk<F, O, FIRST>(dw, a, __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(c)),
+            sum_chunk<F, O, FIRST, kChunk>(
+                dw, a, __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(c)),
                                    static_cast<uint32_t>(col), n);
         } else {
             if constexpr (FIRST)
-                zero_rows<O>(dw, a, static_cast<uint32_t>(b - sum_blocks), per_row);
+                zero_rows<O>(dw, a, static_cast<uint32_t>(b - sum_blocks));
         }
     }
 }
 
-// Runs that cross chunks: the block of the chunk where such a run starts adds its
-// partial rows (slot 1 of that chunk, slot 0 of the following ones), each wave a
-// consecutive share of them, then the waves' sums in order.  blockIdx.y: slices.
+// acc[0..4) += parts [p0, p1) of the run that starts in chunk c: slot 1 of that chunk,
+// slot 0 of the following ones, in order, eight in flight.
+__device__ __forceinline__ void add_parts(float acc[4], const RowSums &a, uint32_t c, uint32_t p0,
+                                          uint32_t p1, uint32_t col) {
+    constexpr uint32_t U = 8;
+    for (uint32_t p = p0; p < p1; p += U) {
+        f32x4 x[U];
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t i = p + u < p1 ? p + u : p1 - 1;
+            x[u] = *reinterpret_cast<const f32x4 *>(
+                part_row(a, static_cast<uint64_t>(c) + i, i == 0 ? 1 : 0, col));
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            if (p + u >= p1) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += x[u][j];
+        }
+    }
+}
+
+// Runs that cross chunks.  A block looks at kJoinChunks chunks and 256 columns (four
+// a lane); a chunk owns the run that starts in it and goes on.  A run of at most
+// kShortRun parts is added by one wave, the waves taking the chunks in turn; a longer
+// one by all waves, each a consecutive share, and then the waves' sums in order.
 template <int O, bool FIRST>
 __global__ __launch_bounds__(kJoinThreads) void join_runs_kernel(elem_t<O> *__restrict__ dw,
-                                                                 RowSums a) {
-    __shared__ float sums[kJoinWaves][kSlice];
+                                                                 RowSums a, uint32_t chunk) {
+    __shared__ float sums[kJoinWaves][kJoinColumns];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63u;
-    const uint32_t c = blockIdx.x, hi = (c + 1) * kChunk;
-    if (hi >= a.tokens) return;
-    const uint32_t key = a.keys[hi - 1];
-    if (key >= a.vocab || a.keys[hi] != key) return;                    // nothing goes on
-    const uint32_t lo = c * kChunk;
-    if (a.keys[lo] == key && lo > 0 && a.keys[lo - 1] == key) return;   // it started before
-    const uint32_t last = lower_bound(a.keys, a.tokens, key + 1) - 1;   // of the run
-    const uint32_t n_part = last / kChunk - c + 1;
-    const uint32_t p0 = static_cast<uint32_t>(static_cast<uint64_t>(n_part) * wave / kJoinWaves);
-    const uint32_t p1 =
-        static_cast<uint32_t>(static_cast<uint64_t>(n_part) * (wave + 1) / kJoinWaves);
-    for (uint32_t s = blockIdx.y; s < a.slices; s += gridDim.y) {
-        const uint32_t col = s * kSlice + lane * 8;
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (col < a.width) {
-            constexpr uint32_t U = 4;
-            for (uint32_t p = p0; p < p1; p += U) {
-                f32x4 x[U][2];
+    const uint32_t c0 = blockIdx.x * kJoinChunks;
+    // lane l: the key of the run that chunk c0 + l owns, or vocab
+    uint32_t own = a.vocab;
+    const uint64_t hi = (static_cast<uint64_t>(c0) + lane + 1) * chunk;
+    if (lane < kJoinChunks && hi < a.tokens) {
+        const uint64_t lo = hi - chunk;
+        const uint32_t key = a.keys[hi - 1], next = a.keys[hi], first = a.keys[lo];
+        const uint32_t prev = lo > 0 ? a.keys[lo - 1] : a.vocab;
+        if (next == key && !(first == key && prev == key)) own = key;
+    }
+    const uint64_t owners = __ballot(own < a.vocab);
+    if (owners == 0) return;
+    for (uint64_t col0 = static_cast<uint64_t>(blockIdx.y) * kJoinColumns; col0 < a.width;
+         col0 += static_cast<uint64_t>(gridDim.y) * kJoinColumns) {
+        const uint32_t col = static_cast<uint32_t>(col0) + lane * 4;
+        const uint32_t n = col >= a.width ? 0u : a.width - col < 4 ? a.width - col : 4u;
+        auto finish = [&](uint32_t key, const float acc[4]) {
+            elem_t<O> *d = dw + static_cast<uint64_t>(key) * a.width + col;
 #pragma unroll
-                for (uint32_t u = 0; u < U; ++u) {
-                    const uint32_t i = p + u < p1 ? p + u : p1 - 1;
-                    const f32x4 *v = reinterpret_cast<const f32x4 *>(
-                        part_row(a, static_cast<uint64_t>(c) + i, i == 0 ? 1 : 0, col));
-                    x[u][0] = v[0];
-                    x[u][1] = v[1];
-                }
-#pragma unroll
-                for (uint32_t u = 0; u < U; ++u) {
-                    if (p + u >= p1) break;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[j] += x[u][j / 4][j % 4];
-                }
+            for (uint32_t j = 0; j < 4; ++j) {
+                if (j >= n) break;
+                const float v = product32(acc[j], a.scale);
+                d[j] = from_f32<O>(FIRST ? v : to_f32<O>(d[j]) + v);
             }
+        };
+        uint64_t longer = 0;
+        uint32_t turn = 0;
+        for (uint64_t m = owners; m != 0; m &= m - 1) {
+            const uint32_t l = static_cast<uint32_t>(__builtin_ctzll(m)), c = c0 + l;
+            const uint32_t key = static_cast<uint32_t>(__builtin_amdgcn_readlane(own, l));
+            // parts of the run, as far as kShortRun tells
+            const uint64_t far = (static_cast<uint64_t>(c) + kShortRun) * chunk;
+            if (far < a.tokens && a.keys[far] == key) {
+                longer |= 1ull << l;
+                continue;
+            }
+            if (turn++ % kJoinWaves != wave) continue;
+            const uint32_t n_part =
+                (wave_lower_bound(a.keys, a.tokens, key + 1) - 1) / chunk - c + 1;
+            float acc[4] = {0, 0, 0, 0};
+            if (n != 0) add_parts(acc, a, c, 0, n_part, col);
+            finish(key, acc);
         }
-        f32x4 *d = reinterpret_cast<f32x4 *>(&sums[wave][lane * 8]);
-        d[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
-        d[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
-        __syncthreads();
-        if (wave == 0 && col < a.width) {
-            for (int w = 1; w < kJoinWaves; ++w)
+        for (uint64_t m = longer; m != 0; m &= m - 1) {
+            const uint32_t l = static_cast<uint32_t>(__builtin_ctzll(m)), c = c0 + l;
+            const uint32_t key = static_cast<uint32_t>(__builtin_amdgcn_readlane(own, l));
+            const uint32_t n_part =
+                (wave_lower_bound(a.keys, a.tokens, key + 1) - 1) / chunk - c + 1;
+            auto share = [&](uint32_t w) {
+                return static_cast<uint32_t>(static_cast<uint64_t>(n_part) * w / kJoinWaves);
+            };
+            float acc[4] = {0, 0, 0, 0};
+            if (n != 0) add_parts(acc, a, c, share(wave), share(wave + 1), col);
+            *reinterpret_cast<f32x4 *>(&sums[wave][lane * 4]) =
+                f32x4{acc[0], acc[1], acc[2], acc[3]};
+            __syncthreads();
+            if (wave == 0) {
+                for (int w = 1; w < kJoinWaves; ++w)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[j] += sums[w][lane * 8 + j];
-            finish_row<O, FIRST>(dw, a, key, col, a.width - col < 8 ? a.width - col : 8, acc);
+                    for (int j = 0; j < 4; ++j) acc[j] += sums[w][lane * 4 + j];
+                finish(key, acc);
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -538,7 +609,13 @@ uint32_t sort_per_block(uint64_t tokens) {
 struct GradSpace {
     uint64_t keys, order, keys2, order2, hist, part, total, ld_part;
     bool rank;
+    uint32_t chunk;
 };
+
+uint32_t chunk_of(uint64_t tokens, uint64_t width) {
+    const uint64_t waves = (tokens + kLongChunk - 1) / kLongChunk * ((width + kSlice - 1) / kSlice);
+    return waves < kFullWaves ? kShortChunk : kLongChunk;
+}
 
 GradSpace grad_space(uint64_t tokens, uint64_t width) {
     GradSpace s{};
@@ -554,25 +631,32 @@ GradSpace grad_space(uint64_t tokens, uint64_t width) {
     }
     s.ld_part = (width + 7) / 8 * 8;
     s.part = at;
-    const uint64_t chunks = (tokens + kChunk - 1) / kChunk;
+    s.chunk = chunk_of(tokens, width);
+    const uint64_t chunks = (tokens + s.chunk - 1) / s.chunk;
     s.total = at + (chunks > 1 ? 8 * s.ld_part * chunks : 0);
     return s;
 }
 
 template <int F, int O, bool FIRST>
-hipError_t sum_rows(void *dw, const RowSums &a, hipStream_t stream) {
+hipError_t sum_rows(void *dw, const RowSums &a, uint32_t chunk, hipStream_t stream) {
     auto *d = static_cast<elem_t<O> *>(dw);
     const uint64_t cap = max_blocks();
     const uint64_t sums =
         (static_cast<uint64_t>(a.chunks) * a.slices + kSumWaves - 1) / kSumWaves;
     const uint64_t zeros = FIRST ? (static_cast<uint64_t>(a.vocab) + kZeroRows - 1) / kZeroRows : 0;
     const uint64_t blocks = sums + zeros < cap ? sums + zeros : cap;
-    chunk_sum_kernel<F, O, FIRST><<<static_cast<uint32_t>(blocks), kSumThreads, 0, stream>>>(
-        d, a, fast_div(a.slices), fast_div((a.width + 7) / 8), sums, zeros);
+    const uint32_t grid = static_cast<uint32_t>(blocks);
+    if (chunk == kLongChunk)
+        chunk_sum_kernel<F, O, FIRST, kLongChunk>
+            <<<grid, kSumThreads, 0, stream>>>(d, a, fast_div(a.slices), sums, zeros);
+    else
+        chunk_sum_kernel<F, O, FIRST, kShortChunk>
+            <<<grid, kSumThreads, 0, stream>>>(d, a, fast_div(a.slices), sums, zeros);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.chunks < 2) return e;
-    const dim3 grid(a.chunks - 1, a.slices < 65535 ? a.slices : 65535);
-    join_runs_kernel<O, FIRST><<<grid, kJoinThreads, 0, stream>>>(d, a);
+    const uint32_t cols = (a.width + kJoinColumns - 1) / kJoinColumns;
+    const dim3 joins((a.chunks + kJoinChunks - 1) / kJoinChunks, cols < 65535 ? cols : 65535);
+    join_runs_kernel<O, FIRST><<<joins, kJoinThreads, 0, stream>>>(d, a, chunk);
     return hipGetLastError();
 }
 
@@ -642,9 +726,9 @@ hipError_t launch_embed_grad(void *dw, bool dw32, bool first, const uint16_t *dy
     }
     const RowSums a{dy, lddy, keys, order, reinterpret_cast<float *>(base + s.part),
                     static_cast<uint32_t>(s.ld_part), T, V, static_cast<uint32_t>(width),
-                    static_cast<uint32_t>((tokens + kChunk - 1) / kChunk),
+                    static_cast<uint32_t>((tokens + s.chunk - 1) / s.chunk),
                     static_cast<uint32_t>((width + kSlice - 1) / kSlice), scale};
-#define ZS_ROWS(F, O, FIRST) return sum_rows<F, O, FIRST>(dw, a, stream)
+#define ZS_ROWS(F, O, FIRST) return sum_rows<F, O, FIRST>(dw, a, s.chunk, stream)
     if (fmt == 0) {
         if (!dw32) ZS_ROWS(0, 0, true);
         if (first) ZS_ROWS(0, 2, true);

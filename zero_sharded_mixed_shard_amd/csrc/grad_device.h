@@ -104,8 +104,8 @@ template <int F>
 __device__ __forceinline__ void store8(elem_t<F> *p, const float v[8]) {
     u32x4_any *d = reinterpret_cast<u32x4_any *>(p);
     if constexpr (F == 2) {
-        __builtin_nontemporal_store(u32x4{bits(v[0]), bits(v[1]), bits(v[2]), bits(v[3])}, d);
-        __builtin_nontemporal_store(u32x4{bits(v[4]), bits(v[5]), bits(v[6]), bits(v[7])}, d + 1);
+        d[0] = u32x4{bits(v[0]), bits(v[1]), bits(v[2]), bits(v[3])};
+        d[1] = u32x4{bits(v[4]), bits(v[5]), bits(v[6]), bits(v[7])};
     } else {
         __builtin_nontemporal_store(u32x4{pack2<F>(v[0], v[1]), pack2<F>(v[2], v[3]),
                                           pack2<F>(v[4], v[5]), pack2<F>(v[6], v[7])}, d);
