@@ -5,8 +5,8 @@ import ctypes
 
 import torch
 
-from ._binding import (_DTYPES, _FORMATS, _ctl_ptr, _f32, _i32, _stream_handle, _u64, _vp,
-                       ZeroError, lib)
+from ._binding import (_DTYPES, _FORMATS, _ctl_ptr, _f32, _i32, _raw_current_stream,
+                       _stream_handle, _u64, _vp, ZeroError, lib)
 
 ACT_BLOCK = 32                                  # ZERO_ACT_BLOCK
 ACT_NONE, ACT_GELU, ACT_SILU = 0, 1, 2          # zero_act
@@ -32,7 +32,13 @@ for _f in ("zero_act_save", "zero_act_load", "zero_act_backward", "zero_weight_g
     getattr(lib, _f).restype = _i32
 
 
-def _on_device(t, name: str, dtypes, device) -> None:
+# The checks below run on every call, so the accepted case is one expression of cheap
+# tests (device index, dtype, shape, strides); what was wrong is worked out afterwards.
+
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _refuse(t, name: str, dtypes, dev, what: str) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -40,60 +46,62 @@ def _on_device(t, name: str, dtypes, device) -> None:
                          "read and write device memory only")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {list(dtypes)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name} must be {what}, got shape {tuple(t.shape)} with strides "
+                     f"{t.stride()}")
 
 
-def _matrix(t, name: str, dtypes, shape=None, device=None) -> tuple:
-    """(pointer, row stride) of a 2-D device tensor with unit column stride."""
-    _on_device(t, name, dtypes, device)
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must have shape {tuple(shape) if shape else '(rows, cols)'}, "
-                         f"got {tuple(t.shape)}")
+def _matrix(t, name: str, dtypes, shape=None, dev=None) -> tuple:
+    """(pointer, row stride) of a 2-D device tensor with unit column stride, of this shape
+    and on this device where they are given."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2 and
+            (dev is None or t.get_device() == dev) and (shape is None or t.shape == shape)):
+        _refuse(t, name, dtypes, dev, f"a matrix of shape {shape or '(rows, cols)'}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        _refuse(t, name, dtypes, dev, "a matrix with unit column stride")
+    return t.data_ptr(), (ld if rows > 1 else cols)
 
 
-def _flat(t, name: str, dtypes, shape, device) -> int:
+def _flat(t, name: str, dtypes, shape, dev) -> int:
     """Pointer of a contiguous device tensor of exactly this shape."""
-    _on_device(t, name, dtypes, device)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and
+            t.get_device() == dev and t.shape == shape and t.is_contiguous()):
+        _refuse(t, name, dtypes, dev, f"contiguous with shape {shape}")
     return t.data_ptr()
 
 
-def _workspace(t, device) -> tuple:
+_U8, _F32 = (torch.uint8,), (torch.float32,)
+
+
+def _workspace(t, dev) -> tuple:
     if t is None:
         return None, 0
-    _on_device(t, "workspace", (torch.uint8,), device)
-    if t.dim() != 1 or not t.is_contiguous():
-        raise ValueError("workspace must be a 1-D contiguous uint8 tensor")
-    return t.data_ptr(), t.numel()
+    n = t.numel() if isinstance(t, torch.Tensor) else 0
+    return _flat(t, "workspace", _U8, (n,), dev), n
 
 
-def _call(name: str, device, stream, *args) -> None:
-    fn = getattr(lib, name)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream_handle(stream, device))
+def _call(name: str, fn, dev: int, stream, *args) -> None:
+    handle = _stream_handle(stream, torch.device("cuda", dev)) if stream is not None or \
+        _raw_current_stream is None else _raw_current_stream(dev)
+    if dev == _get_device():
+        rc = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream_handle(stream, device))
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
     if rc != 0:
         raise ZeroError(rc, name)
 
 
-def _checkpoint(q, e, device) -> tuple:
-    """(q pointer, e pointer, rows, cols) of a checkpoint."""
-    _on_device(q, "q", (torch.uint8,), device)
-    if q.dim() != 2:
-        raise ValueError(f"q must have shape (rows, cols), got {tuple(q.shape)}")
-    rows, cols = q.shape
-    p_q = _flat(q, "q", (torch.uint8,), (rows, cols), device)
-    p_e = _flat(e, "e", (torch.uint8,), (rows, -(-cols // ACT_BLOCK)), device)
-    return p_q, p_e, rows, cols
+def _checkpoint(q, e, dev) -> tuple:
+    """(q pointer, e pointer, shape) of a checkpoint."""
+    if not (isinstance(q, torch.Tensor) and q.dim() == 2):
+        _refuse(q, "q", _U8, dev, "a matrix of shape (rows, cols)")
+    shape = q.shape
+    return (_flat(q, "q", _U8, shape, dev),
+            _flat(e, "e", _U8, (shape[0], -(-shape[1] // ACT_BLOCK)), dev), shape)
 
 
 # ---- 8-bit activation checkpoints -------------------------------------------------
@@ -103,37 +111,39 @@ def zero_act_save(q: torch.Tensor, e: torch.Tensor, x: torch.Tensor, act: int = 
     """Write x's checkpoint: q[rows, cols] and e[rows, ceil(cols/32)], uint8.  With an
     activation function also y = act(x); y may be x."""
     p_x, ldx = _matrix(x, "x", _FORMATS)
-    dev, (rows, cols) = x.device, x.shape
-    p_q, p_e, *shape = _checkpoint(q, e, dev)
-    if shape != [rows, cols]:
-        raise ValueError(f"q must have x's shape {(rows, cols)}, got {tuple(shape)}")
-    p_y, ldy = (None, 0) if y is None else _matrix(y, "y", (x.dtype,), x.shape, dev)
+    dev, shape = x.get_device(), x.shape
+    p_q, p_e, held = _checkpoint(q, e, dev)
+    if held != shape:
+        raise ValueError(f"q must have x's shape {tuple(shape)}, got {tuple(held)}")
     if act != ACT_NONE and y is None:
         raise ValueError("an activation function needs y")
-    _call("zero_act_save", dev, stream, p_q, p_e, p_y, ldy, p_x, ldx, _FORMATS[x.dtype], act,
-          rows, cols)
+    p_y, ldy = (None, 0) if y is None else _matrix(y, "y", (x.dtype,), shape, dev)
+    _call("zero_act_save", lib.zero_act_save, dev, stream, p_q, p_e, p_y, ldy, p_x, ldx,
+          _FORMATS[x.dtype], act, shape[0], shape[1])
 
 
 def zero_act_load(x: torch.Tensor, q: torch.Tensor, e: torch.Tensor, stream=None) -> None:
     """x = the values the checkpoint (q, e) stands for."""
     p_x, ldx = _matrix(x, "x", _FORMATS)
-    p_q, p_e, rows, cols = _checkpoint(q, e, x.device)
-    if tuple(x.shape) != (rows, cols):
-        raise ValueError(f"x must have q's shape {(rows, cols)}, got {tuple(x.shape)}")
-    _call("zero_act_load", x.device, stream, p_x, ldx, _FORMATS[x.dtype], p_q, p_e, rows, cols)
+    dev = x.get_device()
+    p_q, p_e, shape = _checkpoint(q, e, dev)
+    if x.shape != shape:
+        raise ValueError(f"x must have q's shape {tuple(shape)}, got {tuple(x.shape)}")
+    _call("zero_act_load", lib.zero_act_load, dev, stream, p_x, ldx, _FORMATS[x.dtype], p_q, p_e,
+          shape[0], shape[1])
 
 
 def zero_act_backward(dx: torch.Tensor, dy: torch.Tensor, q: torch.Tensor, e: torch.Tensor,
                       act: int, stream=None) -> None:
     """dx = dy * act'(v), v the checkpoint's values; dx may be dy."""
     p_dy, lddy = _matrix(dy, "dy", _FORMATS)
-    dev = dy.device
-    p_q, p_e, rows, cols = _checkpoint(q, e, dev)
-    if tuple(dy.shape) != (rows, cols):
-        raise ValueError(f"dy must have q's shape {(rows, cols)}, got {tuple(dy.shape)}")
-    p_dx, lddx = _matrix(dx, "dx", (dy.dtype,), dy.shape, dev)
-    _call("zero_act_backward", dev, stream, p_dx, lddx, p_dy, lddy, _FORMATS[dy.dtype], act, p_q,
-          p_e, rows, cols)
+    dev = dy.get_device()
+    p_q, p_e, shape = _checkpoint(q, e, dev)
+    if dy.shape != shape:
+        raise ValueError(f"dy must have q's shape {tuple(shape)}, got {tuple(dy.shape)}")
+    p_dx, lddx = _matrix(dx, "dx", (dy.dtype,), shape, dev)
+    _call("zero_act_backward", lib.zero_act_backward, dev, stream, p_dx, lddx, p_dy, lddy,
+          _FORMATS[dy.dtype], act, p_q, p_e, shape[0], shape[1])
 
 
 def _workspace_bytes(name: str, *extents) -> int:
@@ -149,23 +159,19 @@ def zero_weight_grad_workspace(tokens: int, n_out: int, n_in: int) -> int:
     return _workspace_bytes("zero_weight_grad_workspace", tokens, n_out, n_in)
 
 
-def _target_dtypes(dtype) -> tuple:
-    return (dtype, torch.float32)
-
-
 def zero_weight_grad(dw: torch.Tensor, dy: torch.Tensor, q: torch.Tensor, e: torch.Tensor,
                      first: bool = True, workspace: torch.Tensor | None = None,
                      stream=None) -> None:
     """dw[n_out, n_in] = (or, FP32 and not first, +=) dy^T v, v the checkpoint's values."""
     p_dy, lddy = _matrix(dy, "dy", _DTYPES)
-    dev, (tokens, n_out) = dy.device, dy.shape
-    p_q, p_e, rows, n_in = _checkpoint(q, e, dev)
+    dev, (tokens, n_out), dt = dy.get_device(), dy.shape, dy.dtype
+    p_q, p_e, (rows, n_in) = _checkpoint(q, e, dev)
     if rows != tokens:
         raise ValueError(f"q holds {rows} tokens, dy {tokens}")
-    p_dw = _flat(dw, "dw", _target_dtypes(dy.dtype), (n_out, n_in), dev)
+    p_dw = _flat(dw, "dw", (dt, torch.float32), (n_out, n_in), dev)
     p_ws, n_ws = _workspace(workspace, dev)
-    _call("zero_weight_grad", dev, stream, p_dw, _FORMATS[dw.dtype], int(bool(first)), p_dy, lddy,
-          _DTYPES[dy.dtype], p_q, p_e, tokens, n_out, n_in, p_ws, n_ws)
+    _call("zero_weight_grad", lib.zero_weight_grad, dev, stream, p_dw, _FORMATS[dw.dtype],
+          int(bool(first)), p_dy, lddy, _DTYPES[dt], p_q, p_e, tokens, n_out, n_in, p_ws, n_ws)
 
 
 # ---- embedding ------------------------------------------------------------------------
@@ -174,14 +180,14 @@ def zero_embed_lookup(out: torch.Tensor, table: torch.Tensor, ids: torch.Tensor,
                       scale: float = 1.0, stream=None) -> None:
     """out[t] = scale * table[ids[t]]; zeros where ids[t] is outside the table."""
     p_out, ldo = _matrix(out, "out", _FORMATS)
-    dev, (tokens, width) = out.device, out.shape
+    dev, (tokens, width), dt = out.get_device(), out.shape, out.dtype
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a 2-D tensor (vocab, width)")
     vocab = table.shape[0]
-    p_t = _flat(table, "table", (out.dtype,), (vocab, width), dev)
+    p_t = _flat(table, "table", (dt,), (vocab, width), dev)
     p_i = _flat(ids, "ids", _ITYPES, (tokens,), dev)
-    _call("zero_embed_lookup", dev, stream, p_out, ldo, p_t, _FORMATS[out.dtype], p_i,
-          _ITYPES[ids.dtype], tokens, vocab, width, scale)
+    _call("zero_embed_lookup", lib.zero_embed_lookup, dev, stream, p_out, ldo, p_t, _FORMATS[dt],
+          p_i, _ITYPES[ids.dtype], tokens, vocab, width, scale)
 
 
 def zero_embed_grad_workspace(tokens: int, vocab: int, width: int) -> int:
@@ -194,15 +200,16 @@ def zero_embed_grad(dw: torch.Tensor, dy: torch.Tensor, ids: torch.Tensor, scale
                     stream=None) -> None:
     """dw[v] = scale * sum of dy[t] over ids[t] == v; FP32 and not first: added to dw's rows."""
     p_dy, lddy = _matrix(dy, "dy", _DTYPES)
-    dev, (tokens, width) = dy.device, dy.shape
+    dev, (tokens, width), dt = dy.get_device(), dy.shape, dy.dtype
     if not isinstance(dw, torch.Tensor) or dw.dim() != 2:
         raise ValueError("dw must be a 2-D tensor (vocab, width)")
     vocab = dw.shape[0]
-    p_dw = _flat(dw, "dw", _target_dtypes(dy.dtype), (vocab, width), dev)
+    p_dw = _flat(dw, "dw", (dt, torch.float32), (vocab, width), dev)
     p_i = _flat(ids, "ids", _ITYPES, (tokens,), dev)
     p_ws, n_ws = _workspace(workspace, dev)
-    _call("zero_embed_grad", dev, stream, p_dw, _FORMATS[dw.dtype], int(bool(first)), p_dy, lddy,
-          _DTYPES[dy.dtype], p_i, _ITYPES[ids.dtype], tokens, vocab, width, scale, p_ws, n_ws)
+    _call("zero_embed_grad", lib.zero_embed_grad, dev, stream, p_dw, _FORMATS[dw.dtype],
+          int(bool(first)), p_dy, lddy, _DTYPES[dt], p_i, _ITYPES[ids.dtype], tokens, vocab, width,
+          scale, p_ws, n_ws)
 
 
 # ---- policy loss ------------------------------------------------------------------------
@@ -210,23 +217,19 @@ def zero_embed_grad(dw: torch.Tensor, dy: torch.Tensor, ids: torch.Tensor, scale
 def _policy(loss, token_loss, logp, logits, targets, advantage, weight, old_logp, ref_logp,
             dlogits, clip_low, clip_high, kl_coef):
     p_z, ld = _matrix(logits, "logits", _FORMATS)
-    dev, (rows, vocab) = logits.device, logits.shape
-    f32 = (torch.float32,)
-
-    def rows_of(t, name):
-        return None if t is None else _flat(t, name, f32, (rows,), dev)
-
+    dev, shape, dt = logits.get_device(), logits.shape, logits.dtype
+    one, rows = (1,), shape[:1]
     p_d, ldd = (None, 0) if dlogits is None else \
-        _matrix(dlogits, "dlogits", (logits.dtype,), logits.shape, dev)
-    for t, name in ((token_loss, "token_loss"), (logp, "logp"), (advantage, "advantage"),
-                    (weight, "weight")):
-        _on_device(t, name, f32, dev)
-    return dev, (_flat(loss, "loss", f32, (1,), dev), rows_of(token_loss, "token_loss"),
-                 rows_of(logp, "logp"), p_d, ldd, p_z, ld, _FORMATS[logits.dtype],
-                 _flat(targets, "targets", _ITYPES, (rows,), dev), _ITYPES[targets.dtype],
-                 rows_of(old_logp, "old_logp"), rows_of(ref_logp, "ref_logp"),
-                 rows_of(advantage, "advantage"), rows_of(weight, "weight"), rows, vocab,
-                 clip_low, clip_high, kl_coef)
+        _matrix(dlogits, "dlogits", (dt,), shape, dev)
+    return dev, (_flat(loss, "loss", _F32, one, dev),
+                 _flat(token_loss, "token_loss", _F32, rows, dev),
+                 _flat(logp, "logp", _F32, rows, dev), p_d, ldd, p_z, ld, _FORMATS[dt],
+                 _flat(targets, "targets", _ITYPES, rows, dev), _ITYPES[targets.dtype],
+                 None if old_logp is None else _flat(old_logp, "old_logp", _F32, rows, dev),
+                 None if ref_logp is None else _flat(ref_logp, "ref_logp", _F32, rows, dev),
+                 _flat(advantage, "advantage", _F32, rows, dev),
+                 _flat(weight, "weight", _F32, rows, dev), shape[0], shape[1], clip_low,
+                 clip_high, kl_coef)
 
 
 def zero_policy_loss(loss: torch.Tensor, token_loss: torch.Tensor, logp: torch.Tensor,
@@ -239,7 +242,7 @@ def zero_policy_loss(loss: torch.Tensor, token_loss: torch.Tensor, logp: torch.T
     times loss_scale; dlogits may be logits."""
     dev, args = _policy(loss, token_loss, logp, logits, targets, advantage, weight, old_logp,
                         ref_logp, dlogits, clip_low, clip_high, kl_coef)
-    _call("zero_policy_loss", dev, stream, *args, loss_scale)
+    _call("zero_policy_loss", lib.zero_policy_loss, dev, stream, *args, loss_scale)
 
 
 def zero_policy_loss_dev(loss: torch.Tensor, token_loss: torch.Tensor, logp: torch.Tensor,
@@ -251,4 +254,5 @@ def zero_policy_loss_dev(loss: torch.Tensor, token_loss: torch.Tensor, logp: tor
     """zero_policy_loss with the loss scale read from the device control block."""
     dev, args = _policy(loss, token_loss, logp, logits, targets, advantage, weight, old_logp,
                         ref_logp, dlogits, clip_low, clip_high, kl_coef)
-    _call("zero_policy_loss_dev", dev, stream, *args, _ctl_ptr(ctl, dev))
+    _call("zero_policy_loss_dev", lib.zero_policy_loss_dev, dev, stream, *args,
+          _ctl_ptr(ctl, logits.device))

@@ -2,17 +2,24 @@
 //
 // A row's softmax needs its maximum and sum before any gradient can be written,
 // so a plain pass structure reads the logits twice.  Here one block takes a row
-// and keeps its logits in registers (raw 16-B vectors, up to kMaxVec a lane:
-// 196,608 16-bit logits at 1024 lanes): every logit is read once and every
-// gradient written once, which is the floor of 2 + 2 bytes an element.  Longer
-// rows (and the loss without gradients) take a running maximum and sum over one
-// pass and, for the gradients, read the row again.
+// and holds its logits on chip (raw 16-B vectors in registers, for the longest
+// rows part of them in LDS): every logit is read once and every gradient written
+// once, which is the floor of 2 + 2 bytes an element.  Block sizes are such that
+// two or more rows share a compute unit, so that one row's loads and stores run
+// under another's arithmetic.  Rows too long for that (and the loss without
+// gradients) take a running maximum and sum over one pass and, for the gradients,
+// read the row again.
 //
-// Rows start anywhere: vectors are taken at the 16-B boundaries of the row, the
-// first and last partial ones element by element (outside the row a vector
-// holds -inf, which adds nothing).  dlogits may be logits: all of a row is in
-// registers before any of it is written, and the two-pass form writes an
-// element after its last read.
+// The arithmetic matters next to the memory: an element takes a packed maximum,
+// two fused multiply-adds and two 2^x.  e^(z - m) is taken as 2^(z log2 e - c) with
+// c = m log2 e rounded: that rounding scales every term and the sum alike, and the
+// log-probability is formed with the same c, so it cancels.
+//
+// Rows start anywhere: vectors are taken at the 16-B boundaries of the row, and the
+// fewer than 2 * 8 elements before the first and after the last whole vector one a
+// lane (lanes without a vector or an element hold -inf, which adds nothing).  dlogits may be logits: all of a row is on
+// chip before any of it is written, and the two-pass form writes an element after
+// its last read.
 #include "grad_device.h"
 
 #pragma clang fp contract(off)
@@ -24,16 +31,50 @@ constexpr float kInf = __builtin_inff();
 
 template <int F> constexpr int kPer = F == 2 ? 4 : 8;   // logits of a 16-B vector
 
-// ex = e^(z - m): FP32 logits take the accurate form, 16-bit ones the hardware's
-// 2^x (gradients are rounded to 16 bits, and a term's share of the sum falls
-// with the same factor as its relative error grows).
-template <int F>
-__device__ __forceinline__ float exp_from(float z, float m) {
-    if constexpr (F == 2)
-        return expf(z - m);
-    else
-        return exp_fast(z - m);
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+
+// e^(z - m), c = m log2 e.
+__device__ __forceinline__ float exp_from(float z, float c) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -c));
 }
+
+// The largest logit, from the bit patterns: non-negative floats order like signed
+// integers, and among negative ones the largest has the smallest unsigned pattern.
+// Both are tracked, two 16-bit logits an instruction.  A positive NaN ends up as the
+// maximum and a negative one reaches the sum, so either way the row becomes NaN.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+template <int F>
+struct MaxBits {
+    u32x2 most{F == 2 ? 0x80000000u : 0x80008000u, 0u}, least{0xffffffffu, 0u};
+    __device__ __forceinline__ void take(uint32_t w) {
+        if constexpr (F == 2) {
+            const int a = static_cast<int>(most.x), b = static_cast<int>(w);
+            most.x = static_cast<uint32_t>(a > b ? a : b);
+            least.x = least.x < w ? least.x : w;
+        } else {
+            most.x = __builtin_bit_cast(
+                uint32_t, __builtin_elementwise_max(__builtin_bit_cast(s16x2, most.x),
+                                                    __builtin_bit_cast(s16x2, w)));
+            least.x = __builtin_bit_cast(
+                uint32_t, __builtin_elementwise_min(__builtin_bit_cast(u16x2, least.x),
+                                                    __builtin_bit_cast(u16x2, w)));
+        }
+    }
+    // as FP32, NaN where a positive NaN was seen
+    __device__ __forceinline__ float value() const {
+        if constexpr (F == 2) {
+            return from_bits(static_cast<int>(most.x) >= 0 ? most.x : least.x);
+        } else {
+            const s16x2 m = __builtin_bit_cast(s16x2, most.x);
+            const u16x2 l = __builtin_bit_cast(u16x2, least.x);
+            const short hi = m.x > m.y ? m.x : m.y;
+            const unsigned short lo = l.x < l.y ? l.x : l.y;
+            return to_f32<F == 2 ? 0 : F>(hi >= 0 ? static_cast<uint16_t>(hi) : lo);
+        }
+    }
+};
 
 template <int F>
 __device__ __forceinline__ void widen_vec(const u32x4 &w, float out[kPer<F>]) {
@@ -57,55 +98,54 @@ __device__ __forceinline__ u32x4 neg_inf_vec() {
     return u32x4{w, w, w, w};
 }
 
-// Vector j of a row: elements j*K - shift .. +K-1 of the row, shift the elements
-// between the 16-B boundary below the row's start and that start.
+// A row as whole vectors from its first 16-B boundary, and at most one edge element
+// a lane: lane l < head holds element l, lane K + l element tail + l of the rest.
 template <int F>
-__device__ __forceinline__ u32x4 row_vec(const elem_t<F> *row, uint32_t shift, uint32_t vocab,
-                                         uint32_t j) {
-    constexpr int K = kPer<F>;
-    const int64_t e0 = static_cast<int64_t>(j) * K - shift;
-    if (e0 >= 0 && e0 + K <= vocab)
-        return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(row + e0));
-    u32x4 r = neg_inf_vec<F>();
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const int64_t e = e0 + i;
-        if (e >= 0 && e < vocab) {
-            if constexpr (F == 2) {
-                r[i] = bits(row[e]);
-            } else {
-                const uint32_t h = row[e];
-                const uint32_t old = r[i / 2];
-                r[i / 2] = i % 2 ? (old & 0xffffu) | (h << 16) : (old & 0xffff0000u) | h;
-            }
-        }
+struct Row {
+    static constexpr uint32_t K = kPer<F>;
+    uint32_t head, n_vec;    // elements before the vectors, whole vectors
+    uint32_t edge;           // lane l's edge element, ~0 if none
+    __device__ __forceinline__ Row(const elem_t<F> *row, uint32_t V, uint32_t l) {
+        const uint32_t to_vec =
+            static_cast<uint32_t>((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 /
+                                  sizeof(elem_t<F>));
+        head = to_vec < V ? to_vec : V;
+        n_vec = (V - head) / K;
+        const uint32_t tail = head + n_vec * K;
+        edge = l < head ? l : l >= K && l < 2 * K && tail + (l - K) < V ? tail + (l - K) : ~0u;
     }
-    return r;
+};
+
+// Vector first + l of a row, `first` the same in every lane (so it goes into the
+// scalar part of the address), l the lane's own.
+template <int F>
+__device__ __forceinline__ u32x4 vec_at(const elem_t<F> *row, uint32_t head, uint32_t first,
+                                        uint32_t l) {
+    const char *base =
+        reinterpret_cast<const char *>(row + head) + static_cast<uint64_t>(first) * 16;
+    asm volatile("" : "+s"(base));   // a scalar base: no address registers a vector
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(base + l * 16));
 }
 
 template <int F>
-__device__ __forceinline__ void store_row_vec(elem_t<F> *row, uint32_t shift, uint32_t vocab,
-                                              uint32_t j, const float v[kPer<F>]) {
+__device__ __forceinline__ void store_vec_at(elem_t<F> *row, uint32_t head, uint32_t first,
+                                             uint32_t l, const float v[kPer<F>]) {
     constexpr int K = kPer<F>;
-    const int64_t e0 = static_cast<int64_t>(j) * K - shift;
-    if (e0 >= 0 && e0 + K <= vocab) {
-        u32x4 w;
+    u32x4 w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = F == 2 ? bits(v[i]) : pack2<F == 2 ? 0 : F>(v[2 * i % K], v[(2 * i + 1) % K]);
-        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any *>(row + e0));
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const int64_t e = e0 + i;
-        if (e >= 0 && e < vocab) row[e] = from_f32<F>(v[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+        w[i] = F == 2 ? bits(v[i]) : pack2<F == 2 ? 0 : F>(v[2 * i % K], v[(2 * i + 1) % K]);
+    char *base = reinterpret_cast<char *>(row + head) + static_cast<uint64_t>(first) * 16;
+    asm volatile("" : "+s"(base));
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any *>(base + l * 16));
 }
+
+// The larger, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
 
 __device__ __forceinline__ float wave_max(float x) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
+    for (int o = 32; o > 0; o >>= 1) x = max_nan(x, __shfl_xor(x, o));
     return x;
 }
 __device__ __forceinline__ float wave_sum(float x) {
@@ -123,24 +163,37 @@ __device__ __forceinline__ float block_reduce(float x, float *red) {
     __syncthreads();
     float r = red[0];
 #pragma unroll
-    for (int w = 1; w < T / 64; ++w) r = MAX ? fmaxf(r, red[w]) : r + red[w];
+    for (int w = 1; w < T / 64; ++w) r = MAX ? max_nan(r, red[w]) : r + red[w];
     __syncthreads();
     return r;
 }
 
 // What a row's gradient needs, the same in every lane.
 struct RowGrad {
-    float m;        // the row's largest logit
+    float c;        // largest logit times log2 e
     float scale;    // -S w g / sum
     float hit;      // S w g, added at the target
 };
 
-// The row's loss from its maximum and sum; lane 0 writes token_loss and logp.
-__device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, float m, float sum,
-                                              float z_target, float w) {
-    const float logp = z_target - m - logf(sum);
+// e^d - 1: its series up to |d| = 1 (the first term left out is below 2^-28 of the
+// sum), the difference beyond, where it cancels no more than one bit.  Written out
+// because it is live beside the whole row: the library's form would push logits out
+// of registers.
+__device__ __forceinline__ float exp_minus_1(float d) {
+    if (!(__builtin_fabsf(d) <= 1.0f)) return exp_fast(d) - 1.0f;
+    float s = 1.0f;
+#pragma unroll
+    for (int n = 12; n >= 2; --n) s = __builtin_fmaf(d * (1.0f / n), s, 1.0f);
+    return d * s;
+}
+
+// The row's loss from c = max log2 e and the sum; lane 0 writes token_loss and logp.
+__device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, float c, float sum,
+                                              float z_target, float w, uint32_t lane) {
+    const float logp =
+        (__builtin_fmaf(z_target, kLog2e, -c) - __builtin_amdgcn_logf(sum)) * kLn2;   // log2
     const float A = a.advantage[t];
-    const float r = a.old_logp != nullptr ? expf(logp - a.old_logp[t]) : 1.0f;
+    const float r = a.old_logp != nullptr ? exp_fast(logp - a.old_logp[t]) : 1.0f;
     const float lo = 1.0f - a.clip_low, hi = 1.0f + a.clip_high;
     float rc = r < lo ? lo : r;
     rc = rc > hi ? hi : rc;
@@ -149,18 +202,17 @@ __device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, f
     const bool cut = (A > 0.0f && r > hi) || (A < 0.0f && r < lo);
     float g = cut ? 0.0f : p0;
     if (a.ref_logp != nullptr && a.kl_coef != 0.0f) {
-        // e^d - d - 1 without cancellation near d = 0: expm1(d) - d
-        const float d = a.ref_logp[t] - logp, em = expm1f(d);
+        const float d = a.ref_logp[t] - logp, em = exp_minus_1(d);
         L = L + a.kl_coef * (em - d);
         g = g - a.kl_coef * em;
     }
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
         a.token_loss[t] = L;
         a.logp[t] = logp;
     }
     const float S = a.loss_scale_dev != nullptr ? *a.loss_scale_dev : a.loss_scale;
-    const float c = S * (w * g);
-    return RowGrad{m, -c / sum, c};
+    const float h = S * (w * g);
+    return RowGrad{c, -h / sum, h};
 }
 
 // The target's logit, NaN for a target outside the vocabulary (at: its index,
@@ -175,139 +227,213 @@ __device__ __forceinline__ float target_logit(const PolicyArgs &a, const elem_t<
     return in ? to_f32<F>(row[v]) : __builtin_nanf("");
 }
 
-template <int F>
-__host__ __device__ __forceinline__ uint32_t shift_of(const elem_t<F> *row) {
-    return static_cast<uint32_t>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(elem_t<F>));
+// This lane's place in the group of T lanes that has its row.
+template <int T>
+__device__ __forceinline__ uint32_t lane_of() {
+    return T == 64 ? threadIdx.x & 63u : threadIdx.x;
 }
 
 // Row t's gradient is zero everywhere.
 template <int F, int T>
 __device__ __forceinline__ void skip_row(const PolicyArgs &a, uint64_t t) {
-    if (threadIdx.x == 0) {
+    const uint32_t lane = lane_of<T>();
+    if (lane == 0) {
         a.token_loss[t] = 0.0f;
         a.logp[t] = 0.0f;
     }
     if (a.dlogits == nullptr) return;
     auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
-    const uint32_t V = static_cast<uint32_t>(a.vocab), shift = shift_of<F>(d);
-    const uint32_t n_vec = static_cast<uint32_t>((static_cast<uint64_t>(shift) + V + kPer<F> - 1) /
-                                                 kPer<F>);
+    const Row<F> r(d, static_cast<uint32_t>(a.vocab), lane);
     const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (uint32_t j = threadIdx.x; j < n_vec; j += T) store_row_vec<F>(d, shift, V, j, zero);
+    for (uint32_t j = 0; j + lane < r.n_vec; j += T)
+        store_vec_at<F>(d, r.head, j, lane, zero);
+    if (r.edge != ~0u) d[r.edge] = from_f32<F>(0.0f);
 }
 
-// Gradients of vector j from its logits.
+// Gradients of vector first + lane from its logits.
 template <int F>
-__device__ __forceinline__ void grad_vec(elem_t<F> *d, uint32_t shift, uint32_t V, uint32_t j,
-                                         const u32x4 &w, const RowGrad &g, uint32_t target) {
-    constexpr int K = kPer<F>;
+__device__ __forceinline__ void grad_vec(elem_t<F> *d, uint32_t head, uint32_t first,
+                                         uint32_t lane, const u32x4 &w, const RowGrad &g,
+                                         uint32_t target) {
+    constexpr uint32_t K = kPer<F>;
     float z[K];
     widen_vec<F>(w, z);
-    const int64_t e0 = static_cast<int64_t>(j) * K - shift;
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-        const float p = exp_from<F>(z[i], g.m) * g.scale;
-        z[i] = e0 + i == static_cast<int64_t>(target) ? p + g.hit : p;
+    for (uint32_t i = 0; i < K; ++i) z[i] = exp_from(z[i], g.c) * g.scale;
+    // the target's place among the vectors (it wraps to none for an edge element)
+    const uint32_t at = target - head;
+    if (at / K - first == lane) {
+#pragma unroll
+        for (uint32_t i = 0; i < K; ++i) z[i] = at % K == i ? z[i] + g.hit : z[i];
     }
-    store_row_vec<F>(d, shift, V, j, z);
+    store_vec_at<F>(d, head, first, lane, z);
 }
 
-// One row a block of T lanes, its logits in registers: N vectors a lane.
-template <int F, int T, int N>
-__global__ __launch_bounds__(T) void policy_row_kernel(PolicyArgs a) {
-    constexpr int K = kPer<F>;
-    __shared__ float red[T / 64];
+template <int F>
+__device__ __forceinline__ void grad_edge(elem_t<F> *d, uint32_t edge, float z, const RowGrad &g,
+                                          uint32_t target) {
+    if (edge == ~0u) return;
+    const float p = exp_from(z, g.c) * g.scale;
+    d[edge] = from_f32<F>(edge == target ? p + g.hit : p);
+}
+
+// A block of 64 lanes a row would be bound by the rate at which blocks start: rows
+// that one wave holds share a block of kShare waves.
+constexpr int kShare = 4;
+template <int T> constexpr int kBlock = T == 64 ? 64 * kShare : T;
+template <int T>
+__device__ __forceinline__ uint64_t first_row() {
+    if constexpr (T == 64)
+        return static_cast<uint64_t>(blockIdx.x) * kShare +
+               __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    else
+        return blockIdx.x;
+}
+template <int T>
+__device__ __forceinline__ uint64_t row_stride() {
+    return static_cast<uint64_t>(gridDim.x) * (T == 64 ? kShare : 1);
+}
+
+// One row a group of T lanes (a block, or one of the waves of a block), its logits on
+// chip: N vectors a lane in registers and L in LDS.
+template <int F, int T, int N, int L>
+__global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) {
+    constexpr int B = 3;                  // vectors on their way to LDS at once
+    static_assert(L % B == 0, "whole batches");
+    __shared__ float red[kBlock<T> / 64];
+    __shared__ u32x4 held[L > 0 ? L : 1][T];
     const uint32_t V = static_cast<uint32_t>(a.vocab);
-    for (uint64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    for (uint64_t t = first_row<T>(); t < a.rows; t += row_stride<T>()) {
+        uint32_t lane = lane_of<T>();  // of the group; opaque, so that nothing made from it
+        asm volatile("" : "+v"(lane)); // is held in registers from row to row
         const float weight = a.weight[t];
         if (weight == 0.0f) {
             skip_row<F, T>(a, t);
             continue;
         }
         const auto *row = static_cast<const elem_t<F> *>(a.logits) + t * a.ld;
-        const uint32_t shift = shift_of<F>(row);
-        const uint32_t n_vec =
-            static_cast<uint32_t>((static_cast<uint64_t>(shift) + V + K - 1) / K);
+        const Row<F> r(row, V, lane);
+        // lane holds vector i * T + lane; n_vec is hidden between the passes, so that their
+        // lane masks are not kept (in registers the logits need)
+        uint32_t n_vec = r.n_vec;
+        auto on = [&](int i) { return static_cast<uint32_t>(i) * T + lane < n_vec; };
+        auto fetch = [&](int i) {
+            u32x4 w = neg_inf_vec<F>();
+            if (on(i)) w = vec_at<F>(row, r.head, i * T, lane);
+            return w;
+        };
+        MaxBits<F> most;
+        auto take = [&](const u32x4 &w) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) most.take(w[k]);
+        };
         u32x4 x[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t j = i * T + threadIdx.x;
-            x[i] = j < n_vec ? row_vec<F>(row, shift, V, j) : neg_inf_vec<F>();
+        for (int i = 0; i < L; i += B) {
+            u32x4 y[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) y[b] = fetch(N + i + b);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                take(y[b]);
+                held[i + b][lane] = y[b];   // read by the same lane only
+            }
         }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = fetch(i);
         uint32_t target;
         const float zt = target_logit<F>(a, row, t, &target);
-        float m = -kInf;
+        const float ze = r.edge != ~0u ? to_f32<F>(row[r.edge]) : -kInf;
+#pragma unroll
+        for (int i = 0; i < N; ++i) take(x[i]);
+        const float c = block_reduce<T, true>(max_nan(most.value(), ze), red) * kLog2e;
+        float s = exp_from(ze, c);
+        auto add = [&](const u32x4 &w) {
+            float z[kPer<F>];
+            widen_vec<F>(w, z);
+#pragma unroll
+            for (int k = 0; k < kPer<F>; ++k) s = s + exp_from(z[k], c);
+        };
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            float z[K];
-            widen_vec<F>(x[i], z);
-#pragma unroll
-            for (int k = 0; k < K; ++k) m = fmaxf(m, z[k]);
-        }
-        m = block_reduce<T, true>(m, red);
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float z[K];
             keep_raw(x[i]);
-            widen_vec<F>(x[i], z);
+            add(x[i]);
+        }
+        // one LDS vector at a time: read ahead, they would push the row out of registers
 #pragma unroll
-            for (int k = 0; k < K; ++k) s = s + exp_from<F>(z[k], m);
+        for (int i = 0; i < L; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            add(held[i][lane]);
         }
         s = block_reduce<T, false>(s, red);
-        const RowGrad g = finish_row(a, t, m, s, zt, weight);
+        const RowGrad g = finish_row(a, t, c, s, zt, weight, lane);
         auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
+        asm volatile("" : "+s"(n_vec));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const uint32_t j = i * T + threadIdx.x;
             keep_raw(x[i]);
-            if (j < n_vec) grad_vec<F>(d, shift, V, j, x[i], g, target);
+            if (on(i)) grad_vec<F>(d, r.head, i * T, lane, x[i], g, target);
         }
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (on(N + i)) grad_vec<F>(d, r.head, (N + i) * T, lane, held[i][lane], g, target);
+        }
+        grad_edge<F>(d, r.edge, ze, g, target);
     }
 }
 
 // One row a block of T lanes in one pass for the loss (running maximum and sum a
 // lane) and, with dlogits, a second for the gradients.
 template <int F, int T>
-__global__ __launch_bounds__(T) void policy_long_kernel(PolicyArgs a) {
+__global__ __launch_bounds__(kBlock<T>) void policy_long_kernel(PolicyArgs a) {
     constexpr int K = kPer<F>;
-    __shared__ float red[T / 64];
+    __shared__ float red[kBlock<T> / 64];
     const uint32_t V = static_cast<uint32_t>(a.vocab);
-    for (uint64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    const uint32_t lane = lane_of<T>();
+    for (uint64_t t = first_row<T>(); t < a.rows; t += row_stride<T>()) {
         const float weight = a.weight[t];
         if (weight == 0.0f) {
             skip_row<F, T>(a, t);
             continue;
         }
         const auto *row = static_cast<const elem_t<F> *>(a.logits) + t * a.ld;
-        const uint32_t shift = shift_of<F>(row);
-        const uint32_t n_vec =
-            static_cast<uint32_t>((static_cast<uint64_t>(shift) + V + K - 1) / K);
+        const Row<F> r(row, V, lane);
         uint32_t target;
         const float zt = target_logit<F>(a, row, t, &target);
-        float m = -kInf, s = 0.0f;
-        for (uint32_t j = threadIdx.x; j < n_vec; j += T) {
-            float z[K];
-            widen_vec<F>(row_vec<F>(row, shift, V, j), z);
-            float vm = z[0];
+        const float ze = r.edge != ~0u ? to_f32<F>(row[r.edge]) : -kInf;
+        // the edge element's term is 1 in units of its own maximum (NaN if it is not finite)
+        float m = ze, c = m == -kInf ? 0.0f : m * kLog2e;   // c = m log2 e, 0 while m is -inf
+        float s = exp_from(ze, c);
+        for (uint32_t j = 0; j + lane < r.n_vec; j += T) {
+            const u32x4 w = vec_at<F>(row, r.head, j, lane);
+            MaxBits<F> most;
 #pragma unroll
-            for (int k = 1; k < K; ++k) vm = fmaxf(vm, z[k]);
-            if (vm > m) {            // the sum so far in units of the new maximum
-                s = m == -kInf ? s : s * exp_from<F>(m, vm);
+            for (int k = 0; k < 4; ++k) most.take(w[k]);
+            const float vm = max_nan(most.value(), m);
+            if (vm != m) {           // the sum so far in units of the new maximum
+                s = m == -kInf ? s : s * exp_from(m, vm * kLog2e);
                 m = vm;
+                c = m * kLog2e;
             }
-            // nothing but -inf so far adds nothing; a NaN still reaches the sum
-            const float base = m == -kInf ? 0.0f : m;
+            float z[K];
+            widen_vec<F>(w, z);
 #pragma unroll
-            for (int k = 0; k < K; ++k) s = s + exp_from<F>(z[k], base);
+            for (int k = 0; k < K; ++k) s = s + exp_from(z[k], c);
         }
-        const float rm = block_reduce<T, true>(m, red);
-        s = block_reduce<T, false>(m == -kInf ? s : s * exp_from<F>(m, rm), red);
-        const RowGrad g = finish_row(a, t, rm, s, zt, weight);
+        const float rm = block_reduce<T, true>(m, red), rc = rm * kLog2e;
+        // a lane's terms were scaled by its own rounded c
+        s = block_reduce<T, false>(
+            m == -kInf ? s : s * __builtin_amdgcn_exp2f(c - rc), red);
+        if (rm == -kInf) s = __builtin_nanf("");   // nothing left to choose from
+        const RowGrad g = finish_row(a, t, rc, s, zt, weight, lane);
         if (a.dlogits == nullptr) continue;
         auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
-        for (uint32_t j = threadIdx.x; j < n_vec; j += T)
-            grad_vec<F>(d, shift, V, j, row_vec<F>(row, shift, V, j), g, target);
+        for (uint32_t j = 0; j + lane < r.n_vec; j += T)
+            grad_vec<F>(d, r.head, j, lane, vec_at<F>(row, r.head, j, lane), g,
+                        target);
+        grad_edge<F>(d, r.edge, ze, g, target);
     }
 }
 
@@ -318,10 +444,19 @@ __global__ __launch_bounds__(kSumThreads) void policy_sum_kernel(
     float *__restrict__ loss, const float *__restrict__ token_loss,
     const float *__restrict__ weight, uint64_t rows) {
     __shared__ double red[kSumThreads];
+    constexpr int U = 8;   // rows in flight a lane
     double s = 0.0;
-    for (uint64_t t = threadIdx.x; t < rows; t += kSumThreads) {
-        const float w = weight[t];
-        if (w != 0.0f) s += static_cast<double>(w) * static_cast<double>(token_loss[t]);
+    for (uint64_t t0 = threadIdx.x; t0 < rows; t0 += U * kSumThreads) {
+        float w[U], l[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint64_t t = t0 + u * kSumThreads;
+            w[u] = t < rows ? weight[t] : 0.0f;
+            l[u] = t < rows ? token_loss[t] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (w[u] != 0.0f) s += static_cast<double>(w[u]) * static_cast<double>(l[u]);
     }
     red[threadIdx.x] = s;
     for (int o = kSumThreads / 2; o > 0; o >>= 1) {
@@ -332,40 +467,35 @@ __global__ __launch_bounds__(kSumThreads) void policy_sum_kernel(
 }
 
 constexpr uint64_t kMaxGrid = 1ull << 21;   // 1024-lane blocks: below 2^32 lanes a launch
-constexpr int kMaxVec = 24;   // vectors a lane of a 1024-lane block holds
 
 template <int F>
 hipError_t policy_rows(const PolicyArgs &a, hipStream_t stream) {
-    uint64_t cap = max_blocks();
-    if (cap > kMaxGrid) cap = kMaxGrid;
-    const uint32_t grid = static_cast<uint32_t>(a.rows < cap ? a.rows : cap);
-    // vectors of a row: rows share the first one's phase when their stride is whole
-    // vectors, and may have any otherwise
-    constexpr uint64_t K = kPer<F>;
-    const uint64_t shift = a.ld % K == 0 ? shift_of<F>(static_cast<const elem_t<F> *>(a.logits))
-                                         : K - 1;
-    const uint64_t n_vec = (shift + a.vocab + K - 1) / K;
-#define ZS_ROW(T, N)                                                                 \
-    if (n_vec <= static_cast<uint64_t>(T) * (N)) {                                   \
-        policy_row_kernel<F, T, N><<<grid, T, 0, stream>>>(a);                       \
-        return hipGetLastError();                                                    \
-    }
+    const uint64_t n_vec = a.vocab / kPer<F>;   // whole vectors of a row at most
+#define ZS_LAUNCH(kernel, T)                                                          \
+    do {                                                                              \
+        const uint64_t per = T == 64 ? kShare : 1, want = (a.rows + per - 1) / per;   \
+        const uint64_t cap = max_blocks() < kMaxGrid ? max_blocks() : kMaxGrid;       \
+        kernel<<<static_cast<uint32_t>(want < cap ? want : cap), kBlock<T>, 0,        \
+                 stream>>>(a);                                                        \
+        return hipGetLastError();                                                     \
+    } while (0)
+#define ZS_ROW(T, N, L) \
+    if (n_vec <= static_cast<uint64_t>(T) * (N + L)) ZS_LAUNCH((policy_row_kernel<F, T, N, L>), T)
     if (a.dlogits != nullptr) {
-        ZS_ROW(64, 2)
-        ZS_ROW(64, 4)
-        ZS_ROW(256, 4)
-        ZS_ROW(256, 8)
-        ZS_ROW(1024, 4)
-        ZS_ROW(1024, 8)
-        ZS_ROW(1024, 16)
-        ZS_ROW(1024, kMaxVec)
+        ZS_ROW(64, 2, 0);
+        ZS_ROW(64, 4, 0);
+        ZS_ROW(256, 4, 0);
+        ZS_ROW(256, 8, 0);
+        ZS_ROW(256, 16, 0);
+        ZS_ROW(512, 16, 0);
+        ZS_ROW(512, 24, 0);
+        ZS_ROW(512, 23, 9);
+        ZS_ROW(1024, 23, 9);
     }
+    if (n_vec <= 64 * 4) ZS_LAUNCH((policy_long_kernel<F, 64>), 64);
+    ZS_LAUNCH((policy_long_kernel<F, 1024>), 1024);
 #undef ZS_ROW
-    if (n_vec <= 64 * 4)
-        policy_long_kernel<F, 64><<<grid, 64, 0, stream>>>(a);
-    else
-        policy_long_kernel<F, 1024><<<grid, 1024, 0, stream>>>(a);
-    return hipGetLastError();
+#undef ZS_LAUNCH
 }
 
 }  // namespace
