@@ -74,32 +74,70 @@ __device__ __forceinline__ s16x4 read_tr(const uint16_t *p) {
         (__attribute__((address_space(3))) s16x4 *)(p));
 }
 
+// A pointer `bytes` past one that is the same in every lane: the base is kept in
+// scalar registers, so an access needs no address registers of its own.
+template <bool WIDE> struct Offset { using T = uint32_t; };
+template <> struct Offset<true> { using T = uint64_t; };
+template <typename T, typename O>
+__device__ __forceinline__ const T *at_offset(const T *base, O bytes) {
+    if constexpr (sizeof(O) == 4) asm volatile("" : "+s"(base));
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes);
+}
+
 enum class Out { k16, k32, kAdd32 };   // 16-bit result, FP32 result, added to FP32
 
 struct GradShape {
     uint64_t lddy;
     uint32_t tokens, n_out, n_in, blocks_in;   // blocks_in: exponent bytes a row
     uint32_t per_split;                        // tokens a split (a multiple of kStep)
-    uint32_t tiles_in;                         // tiles along n_in
-    uint64_t tiles;
+    uint32_t tiles_out, tiles_in;
+    uint32_t group_i;                          // tiles a group has along n_in, 0: no groups
+    uint64_t work;                             // work items: tiles, or places in groups
 };
 
+// Tile of work item w: tiles in groups of `group_o` x `group_i` (32), groups dealt to
+// the eight XCDs in turn (workgroups go round them by number), so that the blocks of an
+// XCD share operands in its L2.  false: no such tile.
+__device__ __forceinline__ bool tile_of(const GradShape &g, uint64_t w, uint32_t *o, uint32_t *i) {
+    if (g.group_i == 0) {
+        *o = static_cast<uint32_t>(w / g.tiles_in);
+        *i = static_cast<uint32_t>(w - static_cast<uint64_t>(*o) * g.tiles_in);
+        return true;
+    }
+    const uint32_t group_o = 32 / g.group_i, groups_in = (g.tiles_in + g.group_i - 1) / g.group_i;
+    const uint64_t k = w >> 3, group = (k >> 5) * 8 + (w & 7);
+    const uint32_t at = static_cast<uint32_t>(k & 31);
+    const uint64_t go = group / groups_in;
+    *o = static_cast<uint32_t>(go) * group_o + at % group_o;
+    *i = static_cast<uint32_t>(group - go * groups_in) * g.group_i + at / group_o;
+    return go * group_o < g.tiles_out && *o < g.tiles_out && *i < g.tiles_in;
+}
+
 // One BM x BN tile of G over one split of the tokens; WM x WN waves.
-template <int F, Out O, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void weight_grad_kernel(
+//
+// Ragged edges.  A thread stages groups of eight columns.  The last group of a row
+// is read eight columns back from the row's end, so it never leaves the row; its
+// columns are the row's last eight, and the epilogue stores only those that no
+// other group holds.  Groups past the row's end read the same columns and store
+// nothing.  TINY (n_out or n_in below 8): element by element.  Tokens past the end
+// of the split are read as its last token and replaced by zeros.
+template <int F, Out O, int BM, int BN, int WM, int WN, bool TINY>
+__global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     void *__restrict__ out, const uint16_t *__restrict__ dy, const uint8_t *__restrict__ q,
     const uint8_t *__restrict__ e, GradShape g) {
     constexpr int kThreads = 64 * WM * WN;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;     // 32x32 results a wave
     constexpr int kRowsA = kThreads * 8 / BM, kRowsB = kThreads * 8 / BN;  // rows a pass
     constexpr int PA = kStep / kRowsA, PB = kStep / kRowsB;                // passes a step
+    constexpr int KK = kStep / 16;                                         // MFMA steps a step
     __shared__ __align__(16) uint16_t sa[2][kStep * BM];
     __shared__ __align__(16) uint16_t sb[2][kStep * BN];
 
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    for (uint64_t tile = blockIdx.x; tile < g.tiles; tile += gridDim.x) {
-    const uint32_t tile_o = static_cast<uint32_t>(tile / g.tiles_in);
-    const uint32_t o0 = tile_o * BM, i0 = static_cast<uint32_t>(tile - static_cast<uint64_t>(tile_o) * g.tiles_in) * BN;
+    for (uint64_t work = blockIdx.x; work < g.work; work += gridDim.x) {
+    uint32_t tile_o, tile_i;
+    if (!tile_of(g, work, &tile_o, &tile_i)) continue;
+    const uint32_t o0 = tile_o * BM, i0 = tile_i * BN;
     const uint64_t t_first = static_cast<uint64_t>(blockIdx.y) * g.per_split;
     const uint32_t t_begin = static_cast<uint32_t>(t_first < g.tokens ? t_first : g.tokens);
     const uint32_t t_end = static_cast<uint32_t>(
@@ -109,42 +147,67 @@ __global__ __launch_bounds__(64 * WM * WN) void weight_grad_kernel(
     // staging: this thread's eight columns and first row of each tile
     const uint32_t ca = threadIdx.x % (BM / 8) * 8, ra = threadIdx.x / (BM / 8);
     const uint32_t cb = threadIdx.x % (BN / 8) * 8, rb = threadIdx.x / (BN / 8);
-    const uint32_t na = o0 + ca >= g.n_out ? 0u : g.n_out - o0 - ca < 8 ? g.n_out - o0 - ca : 8u;
-    const uint32_t nb = i0 + cb >= g.n_in ? 0u : g.n_in - i0 - cb < 8 ? g.n_in - i0 - cb : 8u;
+    const uint32_t na = TINY ? (o0 + ca < g.n_out ? g.n_out - o0 - ca : 0u) : 8u;
+    const uint32_t nb = TINY ? (i0 + cb < g.n_in ? g.n_in - i0 - cb : 0u) : 8u;
+    const uint32_t col_a = TINY || o0 + ca + 8 <= g.n_out ? o0 + ca : g.n_out - 8;
+    const uint32_t col_b = TINY || i0 + cb + 8 <= g.n_in ? i0 + cb : g.n_in - 8;
+    const uint32_t blk_b = (i0 + cb < g.n_in ? i0 + cb : g.n_in - 1) / ZERO_ACT_BLOCK;
+    // offsets of a lane from a row's start that is the same in every lane: 32 bits
+    // (the launcher checks that kStep rows stay below 4 GiB; TINY takes any)
+    using Off = typename Offset<TINY>::T;
     u32x4 xa[PA];
     u32x2 xb[PB];
     uint32_t eb[PB];
-    auto load = [&](uint32_t t0) {
+    auto get_a = [&](const uint16_t *row, Off off) {
+        const uint16_t *s = at_offset(row, off * 2);
+        if constexpr (!TINY) return *reinterpret_cast<const u32x4_any *>(s);
+        u32x4 r{0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int p = 0; p < PA; ++p) {
-            const uint32_t t = t0 + ra + p * kRowsA;
-            xa[p] = u32x4{0u, 0u, 0u, 0u};
-            if (t < t_end) {
-                const uint16_t *s = dy + static_cast<uint64_t>(t) * g.lddy + o0 + ca;
-                if (na == 8) {
-                    xa[p] = *reinterpret_cast<const u32x4_any *>(s);
-                } else {
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < na) r[j / 2] |= static_cast<uint32_t>(s[j]) << (16 * (j % 2));
+        return r;
+    };
+    auto get_b = [&](const uint8_t *row, Off off) {
+        const uint8_t *s = at_offset(row, off);
+        if constexpr (!TINY) return *reinterpret_cast<const u32x2_any *>(s);
+        u32x2 r{0u, 0u};
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j)
-                        if (j < na) xa[p][j / 2] |= static_cast<uint32_t>(s[j]) << (16 * (j % 2));
-                }
+        for (uint32_t j = 0; j < 8; ++j)
+            if (j < nb) r[j / 4] |= static_cast<uint32_t>(s[j]) << (8 * (j % 4));
+        return r;
+    };
+    const Off off_a = static_cast<Off>(ra) * static_cast<Off>(g.lddy) + col_a;
+    const Off off_b = static_cast<Off>(rb) * g.n_in + col_b;
+    const Off off_e = static_cast<Off>(rb) * g.blocks_in + blk_b;
+    // step s into registers; the last step may be short
+    auto load = [&](uint32_t s) {
+        const uint32_t t0 = t_begin + s * kStep;
+        const uint16_t *row_a = dy + static_cast<uint64_t>(t0) * g.lddy;
+        const uint8_t *row_b = q + static_cast<uint64_t>(t0) * g.n_in;
+        const uint8_t *row_e = e + static_cast<uint64_t>(t0) * g.blocks_in;
+        if (t0 + kStep <= t_end) {
+#pragma unroll
+            for (int p = 0; p < PA; ++p)
+                xa[p] = get_a(row_a + static_cast<uint64_t>(p * kRowsA) * g.lddy, off_a);
+#pragma unroll
+            for (int p = 0; p < PB; ++p) {
+                xb[p] = get_b(row_b + static_cast<uint64_t>(p * kRowsB) * g.n_in, off_b);
+                eb[p] = *at_offset(row_e + static_cast<uint64_t>(p * kRowsB) * g.blocks_in, off_e);
             }
-        }
+        } else {
+            const uint32_t last = t_end - 1 - t0;
 #pragma unroll
-        for (int p = 0; p < PB; ++p) {
-            const uint32_t t = t0 + rb + p * kRowsB;
-            xb[p] = u32x2{0u, 0u};
-            eb[p] = 127u;
-            if (t < t_end && nb != 0) {
-                const uint8_t *s = q + static_cast<uint64_t>(t) * g.n_in + i0 + cb;
-                eb[p] = e[static_cast<uint64_t>(t) * g.blocks_in + (i0 + cb) / ZERO_ACT_BLOCK];
-                if (nb == 8) {
-                    xb[p] = *reinterpret_cast<const u32x2_any *>(s);
-                } else {
+            for (int p = 0; p < PA; ++p) {
+                const uint32_t t = ra + p * kRowsA, u = t < last ? t : last;
+                xa[p] = get_a(row_a, static_cast<Off>(u) * static_cast<Off>(g.lddy) + col_a);
+                if (t > last) xa[p] = u32x4{0u, 0u, 0u, 0u};
+            }
 #pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j)
-                        if (j < nb) xb[p][j / 4] |= static_cast<uint32_t>(s[j]) << (8 * (j % 4));
-                }
+            for (int p = 0; p < PB; ++p) {
+                const uint32_t t = rb + p * kRowsB, u = t < last ? t : last;
+                xb[p] = get_b(row_b, static_cast<Off>(u) * g.n_in + col_b);
+                eb[p] = *at_offset(row_e, static_cast<Off>(u) * g.blocks_in + blk_b);
+                if (t > last) xb[p] = u32x2{0u, 0u};
             }
         }
     };
@@ -173,6 +236,21 @@ __global__ __launch_bounds__(64 * WM * WN) void weight_grad_kernel(
 #pragma unroll
     for (int n = 0; n < TN; ++n)
         pb[n] = place(half * 8 + (j >> 2), bn + n * 32 + grp * 16 + (j & 3u) * 4, BN);
+    s16x8 a[2][TM], b[2][TN];
+    auto read = [&](int f, uint32_t buf, int kk) {
+#pragma unroll
+        for (int m = 0; m < TM; ++m) {
+            const s16x4 lo = read_tr(&sa[buf][pa[m] + kk * 16 * BM]);
+            const s16x4 hi = read_tr(&sa[buf][pa[m] + (kk * 16 + 4) * BM]);
+            a[f][m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+            const s16x4 lo = read_tr(&sb[buf][pb[n] + kk * 16 * BN]);
+            const s16x4 hi = read_tr(&sb[buf][pb[n] + (kk * 16 + 4) * BN]);
+            b[f][n] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
 
     f32x16 acc[TM][TN];
 #pragma unroll
@@ -183,51 +261,66 @@ __global__ __launch_bounds__(64 * WM * WN) void weight_grad_kernel(
             for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.0f;
 
     if (steps > 0) {
-        load(t_begin);
+        load(0);
         stage(0);
-        if (steps > 1) load(t_begin + kStep);
+        if (steps > 1) load(1);
         __syncthreads();
+        read(0, 0, 0);
     }
-    for (uint32_t s = 0; s < steps; ++s) {
-        const uint32_t buf = s & 1u;
-        if (s + 1 < steps) {
-            stage(buf ^ 1u);
-            if (s + 2 < steps) load(t_begin + (s + 2) * kStep);
-        }
+    // A step: fragments one MFMA step ahead; the next step's tiles go to LDS beside the
+    // first MFMA step, and the one after that is requested from memory.  The barrier
+    // stands where every wave has this buffer's last fragments in registers and its
+    // share of the next buffer written: behind it the next buffer may be read and
+    // this one be overwritten.
+    auto step = [&](uint32_t s, uint32_t buf) {
+        const bool more = s + 1 < steps;
 #pragma unroll
-        for (uint32_t k = 0; k < kStep; k += 16) {
-            s16x8 a[TM], b[TN];
-#pragma unroll
-            for (int m = 0; m < TM; ++m) {
-                const s16x4 lo = read_tr(&sa[buf][pa[m] + k * BM]);
-                const s16x4 hi = read_tr(&sa[buf][pa[m] + (k + 4) * BM]);
-                a[m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        for (int kk = 0; kk < KK; ++kk) {
+            if (kk + 1 < KK) {
+                read((kk + 1) & 1, buf, kk + 1);
+            } else {
+                __syncthreads();
+                if (more) read(0, buf ^ 1u, 0);
             }
-#pragma unroll
-            for (int n = 0; n < TN; ++n) {
-                const s16x4 lo = read_tr(&sb[buf][pb[n] + k * BN]);
-                const s16x4 hi = read_tr(&sb[buf][pb[n] + (k + 4) * BN]);
-                b[n] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            if (kk == 0 && more) {
+                stage(buf ^ 1u);
+                if (s + 2 < steps) load(s + 2);
             }
 #pragma unroll
             for (int m = 0; m < TM; ++m)
 #pragma unroll
-                for (int n = 0; n < TN; ++n) acc[m][n] = mfma<F>(a[m], b[n], acc[m][n]);
+                for (int n = 0; n < TN; ++n)
+                    acc[m][n] = mfma<F>(a[kk & 1][m], b[kk & 1][n], acc[m][n]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __syncthreads();
+    };
+    for (uint32_t s = 0; s < steps; s += 2) {
+        step(s, 0);
+        if (s + 1 < steps) step(s + 1, 1);
     }
 
-    // result register r of a lane: row 8 (r/4) + 4 half + r%4, column lane mod 32
+    // result register r of a lane: row 8 (r/4) + 4 half + r%4, column lane mod 32;
+    // positions of the last group stand for the row's last eight columns
+    auto column = [](uint32_t at, uint32_t first, uint32_t n) {   // ~0: not this one's to store
+        const uint32_t c = first + at;
+        if (TINY || first + (at | 7u) < n) return c < n ? c : ~0u;
+        const uint32_t group = c & ~7u;
+        if (group >= n) return ~0u;
+        const uint32_t real = n - 8 + (c & 7u);
+        return real >= group ? real : ~0u;
+    };
     const uint64_t plane = static_cast<uint64_t>(g.n_out) * g.n_in;
 #pragma unroll
-    for (int m = 0; m < TM; ++m)
+    for (int n = 0; n < TN; ++n) {
+        const uint32_t col = column(bn + n * 32 + (lane & 31u), i0, g.n_in);
 #pragma unroll
-        for (int n = 0; n < TN; ++n) {
-            const uint32_t col = i0 + bn + n * 32 + (lane & 31u);
+        for (int m = 0; m < TM; ++m) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const uint32_t row = o0 + am + m * 32 + 8 * (r / 4) + 4 * half + r % 4;
-                if (row < g.n_out && col < g.n_in) {
+                __builtin_amdgcn_sched_barrier(0);
+                const uint32_t row = column(am + m * 32 + 8 * (r / 4) + 4 * half + r % 4, o0,
+                                            g.n_out);
+                if (row != ~0u && col != ~0u) {
                     const uint64_t at = static_cast<uint64_t>(row) * g.n_in + col;
                     if constexpr (O == Out::k16) {
                         static_cast<uint16_t *>(out)[at] = from_f32<F>(acc[m][n][r]);
@@ -238,6 +331,8 @@ __global__ __launch_bounds__(64 * WM * WN) void weight_grad_kernel(
                 }
             }
         }
+    }
+    __syncthreads();   // the next tile writes LDS
     }
 }
 
@@ -280,6 +375,7 @@ struct Plan {
 };
 
 constexpr uint64_t kFill = 256;   // compute units of the chip
+constexpr uint64_t kMaxStride = 1ull << 24;   // kStep rows and a row's columns below 2^32 bytes
 
 Plan plan_of(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
     auto tiles = [&](uint64_t b) { return ((n_out + b - 1) / b) * ((n_in + b - 1) / b); };
@@ -297,21 +393,24 @@ Plan plan_of(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
 
 template <int F, Out O>
 hipError_t tiles_of(void *out, const uint16_t *dy, const uint8_t *q, const uint8_t *e,
-                    const GradShape &g, const Plan &p, hipStream_t stream) {
+                    const GradShape &g, const Plan &p, bool tiny, hipStream_t stream) {
     const uint64_t cap = max_blocks();
-    const dim3 grid(static_cast<uint32_t>(g.tiles < cap ? g.tiles : cap), p.splits);
-    if (p.big)
-        weight_grad_kernel<F, O, 256, 256, 4, 2><<<grid, 512, 0, stream>>>(out, dy, q, e, g);
+    const dim3 grid(static_cast<uint32_t>(g.work < cap ? g.work : cap), p.splits);
+    if (tiny)
+        weight_grad_kernel<F, O, 128, 128, 2, 2, true><<<grid, 256, 0, stream>>>(out, dy, q, e, g);
+    else if (p.big)
+        weight_grad_kernel<F, O, 256, 256, 4, 2, false><<<grid, 512, 0, stream>>>(out, dy, q, e, g);
     else
-        weight_grad_kernel<F, O, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(out, dy, q, e, g);
+        weight_grad_kernel<F, O, 128, 128, 2, 2, false><<<grid, 256, 0, stream>>>(out, dy, q, e, g);
     return hipGetLastError();
 }
 
 template <int F, Out O>
 hipError_t grad_as(void *dw, const uint16_t *dy, const uint8_t *q, const uint8_t *e,
-                   const GradShape &g, const Plan &p, void *workspace, hipStream_t stream) {
-    if (p.splits == 1) return tiles_of<F, O>(dw, dy, q, e, g, p, stream);
-    const hipError_t err = tiles_of<F, Out::k32>(workspace, dy, q, e, g, p, stream);
+                   const GradShape &g, const Plan &p, bool tiny, void *workspace,
+                   hipStream_t stream) {
+    if (p.splits == 1) return tiles_of<F, O>(dw, dy, q, e, g, p, tiny, stream);
+    const hipError_t err = tiles_of<F, Out::k32>(workspace, dy, q, e, g, p, tiny, stream);
     if (err != hipSuccess) return err;
     const uint64_t n = static_cast<uint64_t>(g.n_out) * g.n_in;
     join_splits_kernel<F, O><<<capped_blocks(n), kJoinThreads, 0, stream>>>(
@@ -331,17 +430,27 @@ hipError_t launch_weight_grad(void *dw, bool dw32, bool first, const uint16_t *d
                               uint64_t n_out, uint64_t n_in, void *workspace,
                               hipStream_t stream) {
     const Plan p = plan_of(tokens, n_out, n_in);
-    const uint64_t b = p.big ? 256 : 128;
-    const uint64_t tiles_in = (n_in + b - 1) / b;
-    const GradShape g{lddy,
-                      static_cast<uint32_t>(tokens),
-                      static_cast<uint32_t>(n_out),
-                      static_cast<uint32_t>(n_in),
-                      static_cast<uint32_t>((n_in + ZERO_ACT_BLOCK - 1) / ZERO_ACT_BLOCK),
-                      p.per_split,
-                      static_cast<uint32_t>(tiles_in),
-                      tiles_in * ((n_out + b - 1) / b)};
-#define ZS_GRAD(F, O) return grad_as<F, O>(dw, dy, q, e, g, p, workspace, stream)
+    const bool tiny = n_out < 8 || n_in < 8 || n_in >= kMaxStride || lddy >= kMaxStride;
+    const uint64_t b = p.big && !tiny ? 256 : 128;
+    const uint64_t tiles_in = (n_in + b - 1) / b, tiles_out = (n_out + b - 1) / b;
+    GradShape g{lddy,
+                static_cast<uint32_t>(tokens),
+                static_cast<uint32_t>(n_out),
+                static_cast<uint32_t>(n_in),
+                static_cast<uint32_t>((n_in + ZERO_ACT_BLOCK - 1) / ZERO_ACT_BLOCK),
+                p.per_split,
+                static_cast<uint32_t>(tiles_out),
+                static_cast<uint32_t>(tiles_in),
+                0,
+                tiles_in * tiles_out};
+    if (g.work >= kFill) {   // fewer tiles than compute units: every XCD gets some as it is
+        g.group_i = tiles_in >= 4 ? 4 : tiles_in >= 2 ? 2 : 1;
+        const uint64_t go = 32 / g.group_i;
+        const uint64_t groups =
+            ((tiles_out + go - 1) / go) * ((tiles_in + g.group_i - 1) / g.group_i);
+        g.work = (groups + 7) / 8 * 8 * 32;
+    }
+#define ZS_GRAD(F, O) return grad_as<F, O>(dw, dy, q, e, g, p, tiny, workspace, stream)
     if (fmt == 0) {
         if (!dw32) ZS_GRAD(0, Out::k16);
         if (first) ZS_GRAD(0, Out::k32);
