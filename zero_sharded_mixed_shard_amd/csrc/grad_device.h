@@ -22,6 +22,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 
+// Global memory by type: a pointer that went through an empty asm statement (to keep it
+// in scalar registers) is not known to be global any more, and would be read by flat
+// instructions.
+#define GLOBAL_AS __attribute__((address_space(1)))
+
 template <int F> struct Elem { using T = uint16_t; };
 template <> struct Elem<2> { using T = float; };
 template <int F> using elem_t = typename Elem<F>::T;

@@ -121,10 +121,9 @@ struct Row {
 template <int F>
 __device__ __forceinline__ u32x4 vec_at(const elem_t<F> *row, uint32_t head, uint32_t first,
                                         uint32_t l) {
-    const char *base =
-        reinterpret_cast<const char *>(row + head) + static_cast<uint64_t>(first) * 16;
+    auto *base = (const GLOBAL_AS char *)(row + head) + static_cast<uint64_t>(first) * 16;
     asm volatile("" : "+s"(base));   // a scalar base: no address registers a vector
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(base + l * 16));
+    return __builtin_nontemporal_load((const GLOBAL_AS u32x4 *)(base + l * 16));
 }
 
 template <int F>
@@ -135,9 +134,9 @@ __device__ __forceinline__ void store_vec_at(elem_t<F> *row, uint32_t head, uint
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         w[i] = F == 2 ? bits(v[i]) : pack2<F == 2 ? 0 : F>(v[2 * i % K], v[(2 * i + 1) % K]);
-    char *base = reinterpret_cast<char *>(row + head) + static_cast<uint64_t>(first) * 16;
+    auto *base = (GLOBAL_AS char *)(row + head) + static_cast<uint64_t>(first) * 16;
     asm volatile("" : "+s"(base));
-    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any *>(base + l * 16));
+    __builtin_nontemporal_store(w, (GLOBAL_AS u32x4_any *)(base + l * 16));
 }
 
 // The larger, NaN if either is.

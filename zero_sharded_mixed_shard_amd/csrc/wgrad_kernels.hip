@@ -79,9 +79,33 @@ __device__ __forceinline__ s16x4 read_tr(const uint16_t *p) {
 template <bool WIDE> struct Offset { using T = uint32_t; };
 template <> struct Offset<true> { using T = uint64_t; };
 template <typename T, typename O>
-__device__ __forceinline__ const T *at_offset(const T *base, O bytes) {
-    if constexpr (sizeof(O) == 4) asm volatile("" : "+s"(base));
-    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + bytes);
+__device__ __forceinline__ const GLOBAL_AS T *at_offset(const T *base, O bytes) {
+    auto *b = (const GLOBAL_AS char *)(base);
+    if constexpr (sizeof(O) == 4) asm volatile("" : "+s"(b));
+    return (const GLOBAL_AS T *)(b + bytes);
+}
+
+// Order of a scheduling region that holds M MFMAs, R LDS reads, V other vector
+// operations, W LDS writes and G memory reads: each kind dealt evenly between the MFMAs.
+template <int I, int M, int R, int V, int W, int G>
+__device__ __forceinline__ void deal() {
+    if constexpr (I < M) {
+        constexpr int kFrom = I, kTo = I + 1;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr (R * kTo / M > R * kFrom / M)
+            __builtin_amdgcn_sched_group_barrier(0x100, R * kTo / M - R * kFrom / M, 0);
+        if constexpr (V * kTo / M > V * kFrom / M)
+            __builtin_amdgcn_sched_group_barrier(0x002, V * kTo / M - V * kFrom / M, 0);
+        if constexpr (W * kTo / M > W * kFrom / M)
+            __builtin_amdgcn_sched_group_barrier(0x200, W * kTo / M - W * kFrom / M, 0);
+        if constexpr (G * kTo / M > G * kFrom / M)
+            __builtin_amdgcn_sched_group_barrier(0x020, G * kTo / M - G * kFrom / M, 0);
+        deal<I + 1, M, R, V, W, G>();
+    }
+}
+template <int M, int R, int V, int W, int G>
+__device__ __forceinline__ void interleave() {
+    deal<0, M, R, V, W, G>();
 }
 
 enum class Out { k16, k32, kAdd32 };   // 16-bit result, FP32 result, added to FP32
@@ -159,8 +183,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     u32x2 xb[PB];
     uint32_t eb[PB];
     auto get_a = [&](const uint16_t *row, Off off) {
-        const uint16_t *s = at_offset(row, off * 2);
-        if constexpr (!TINY) return *reinterpret_cast<const u32x4_any *>(s);
+        const GLOBAL_AS uint16_t *s = at_offset(row, off * 2);
+        if constexpr (!TINY) return *(const GLOBAL_AS u32x4_any *)(s);
         u32x4 r{0u, 0u, 0u, 0u};
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j)
@@ -168,8 +192,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
         return r;
     };
     auto get_b = [&](const uint8_t *row, Off off) {
-        const uint8_t *s = at_offset(row, off);
-        if constexpr (!TINY) return *reinterpret_cast<const u32x2_any *>(s);
+        const GLOBAL_AS uint8_t *s = at_offset(row, off);
+        if constexpr (!TINY) return *(const GLOBAL_AS u32x2_any *)(s);
         u32x2 r{0u, 0u};
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j)
@@ -179,46 +203,58 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     const Off off_a = static_cast<Off>(ra) * static_cast<Off>(g.lddy) + col_a;
     const Off off_b = static_cast<Off>(rb) * g.n_in + col_b;
     const Off off_e = static_cast<Off>(rb) * g.blocks_in + blk_b;
-    // step s into registers; the last step may be short
+    // step s into registers: a whole step, or (load_last) the last, perhaps short, one
+    auto load_a = [&](uint32_t s) {
+        const uint16_t *row = dy + static_cast<uint64_t>(t_begin + s * kStep) * g.lddy;
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+            xa[p] = get_a(row + static_cast<uint64_t>(p * kRowsA) * g.lddy, off_a);
+    };
+    auto load_b = [&](uint32_t s) {
+        const uint64_t t0 = t_begin + s * kStep;
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+            xb[p] = get_b(q + (t0 + p * kRowsB) * g.n_in, off_b);
+            eb[p] = *at_offset(e + (t0 + p * kRowsB) * g.blocks_in, off_e);
+        }
+    };
+    auto load_last = [&](uint32_t s) {
+        const uint32_t t0 = t_begin + s * kStep, last = t_end - 1 - t0;
+#pragma unroll
+        for (int p = 0; p < PA; ++p) {
+            const uint32_t t = ra + p * kRowsA, u = t < last ? t : last;
+            xa[p] = get_a(dy + static_cast<uint64_t>(t0) * g.lddy,
+                          static_cast<Off>(u) * static_cast<Off>(g.lddy) + col_a);
+            if (t > last) xa[p] = u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+            const uint32_t t = rb + p * kRowsB, u = t < last ? t : last;
+            xb[p] = get_b(q + static_cast<uint64_t>(t0) * g.n_in,
+                          static_cast<Off>(u) * g.n_in + col_b);
+            eb[p] = *at_offset(e + static_cast<uint64_t>(t0) * g.blocks_in,
+                               static_cast<Off>(u) * g.blocks_in + blk_b);
+            if (t > last) xb[p] = u32x2{0u, 0u};
+        }
+    };
     auto load = [&](uint32_t s) {
-        const uint32_t t0 = t_begin + s * kStep;
-        const uint16_t *row_a = dy + static_cast<uint64_t>(t0) * g.lddy;
-        const uint8_t *row_b = q + static_cast<uint64_t>(t0) * g.n_in;
-        const uint8_t *row_e = e + static_cast<uint64_t>(t0) * g.blocks_in;
-        if (t0 + kStep <= t_end) {
-#pragma unroll
-            for (int p = 0; p < PA; ++p)
-                xa[p] = get_a(row_a + static_cast<uint64_t>(p * kRowsA) * g.lddy, off_a);
-#pragma unroll
-            for (int p = 0; p < PB; ++p) {
-                xb[p] = get_b(row_b + static_cast<uint64_t>(p * kRowsB) * g.n_in, off_b);
-                eb[p] = *at_offset(row_e + static_cast<uint64_t>(p * kRowsB) * g.blocks_in, off_e);
-            }
+        if (s + 1 == steps) {
+            load_last(s);
         } else {
-            const uint32_t last = t_end - 1 - t0;
-#pragma unroll
-            for (int p = 0; p < PA; ++p) {
-                const uint32_t t = ra + p * kRowsA, u = t < last ? t : last;
-                xa[p] = get_a(row_a, static_cast<Off>(u) * static_cast<Off>(g.lddy) + col_a);
-                if (t > last) xa[p] = u32x4{0u, 0u, 0u, 0u};
-            }
-#pragma unroll
-            for (int p = 0; p < PB; ++p) {
-                const uint32_t t = rb + p * kRowsB, u = t < last ? t : last;
-                xb[p] = get_b(row_b, static_cast<Off>(u) * g.n_in + col_b);
-                eb[p] = *at_offset(row_e, static_cast<Off>(u) * g.blocks_in + blk_b);
-                if (t > last) xb[p] = u32x2{0u, 0u};
-            }
+            load_a(s);
+            load_b(s);
         }
     };
     // LDS place of eight columns c of row r in a tile of `width` columns
     auto place = [](uint32_t r, uint32_t c, uint32_t width) {
         return r * width + (((c >> 4) ^ ((r & 3u) << 1)) << 4) + (c & 15u);
     };
-    auto stage = [&](uint32_t buf) {
+    auto stage_a = [&](uint32_t buf) {
 #pragma unroll
         for (int p = 0; p < PA; ++p)
             *reinterpret_cast<u32x4 *>(&sa[buf][place(ra + p * kRowsA, ca, BM)]) = xa[p];
+    };
+    auto stage_b = [&](uint32_t buf) {
 #pragma unroll
         for (int p = 0; p < PB; ++p)
             *reinterpret_cast<u32x4 *>(&sb[buf][place(rb + p * kRowsB, cb, BN)]) =
@@ -260,18 +296,53 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.0f;
 
+    auto multiply = [&](int f) {
+#pragma unroll
+        for (int m = 0; m < TM; ++m)
+#pragma unroll
+            for (int n = 0; n < TN; ++n) acc[m][n] = mfma<F>(a[f][m], b[f][n], acc[m][n]);
+    };
+
     if (steps > 0) {
         load(0);
-        stage(0);
+        stage_a(0);
+        stage_b(0);
         if (steps > 1) load(1);
         __syncthreads();
         read(0, 0, 0);
     }
     // A step: fragments one MFMA step ahead; the next step's tiles go to LDS beside the
-    // first MFMA step, and the one after that is requested from memory.  The barrier
-    // stands where every wave has this buffer's last fragments in registers and its
-    // share of the next buffer written: behind it the next buffer may be read and
-    // this one be overwritten.
+    // first two MFMA steps, and the ones after that are requested from memory as their
+    // registers become free.  The barrier stands where every wave has this buffer's last
+    // fragments in registers and its share of the next buffer written: behind it the next
+    // buffer may be read and this one be overwritten.
+    //
+    // Steady state, free of branches so that each MFMA step is one scheduling region: a
+    // wave's LDS reads, conversions, LDS writes and requests are dealt between its MFMAs.
+    constexpr int kMfma = TM * TN, kReads = 2 * (TM + TN);
+    auto steady = [&](uint32_t s, uint32_t buf) {
+        static_assert(KK == 4, "the barrier stands before the last MFMA step");
+        read(1, buf, 1);
+        multiply(0);
+        stage_a(buf ^ 1u);
+        load_a(s + 2);
+        interleave<kMfma, kReads, 0, PA, PA>();
+        __builtin_amdgcn_sched_barrier(0);
+        read(0, buf, 2);
+        multiply(1);
+        stage_b(buf ^ 1u);
+        load_b(s + 2);
+        interleave<kMfma, kReads, 12 * PB, PB, 2 * PB>();
+        __builtin_amdgcn_sched_barrier(0);
+        read(1, buf, 3);
+        multiply(0);
+        interleave<kMfma, kReads, 0, 0, 0>();
+        __syncthreads();
+        read(0, buf ^ 1u, 0);
+        multiply(1);
+        interleave<kMfma, kReads, 0, 0, 0>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
     auto step = [&](uint32_t s, uint32_t buf) {
         const bool more = s + 1 < steps;
 #pragma unroll
@@ -283,21 +354,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
                 if (more) read(0, buf ^ 1u, 0);
             }
             if (kk == 0 && more) {
-                stage(buf ^ 1u);
+                stage_a(buf ^ 1u);
+                stage_b(buf ^ 1u);
                 if (s + 2 < steps) load(s + 2);
             }
-#pragma unroll
-            for (int m = 0; m < TM; ++m)
-#pragma unroll
-                for (int n = 0; n < TN; ++n)
-                    acc[m][n] = mfma<F>(a[kk & 1][m], b[kk & 1][n], acc[m][n]);
-            __builtin_amdgcn_sched_barrier(0);
+            multiply(kk & 1);
         }
     };
-    for (uint32_t s = 0; s < steps; s += 2) {
-        step(s, 0);
-        if (s + 1 < steps) step(s + 1, 1);
+    uint32_t s = 0;
+    for (; s + 4 < steps; s += 2) {   // steps s + 2 and s + 3 are whole
+        steady(s, 0);
+        steady(s + 1, 1);
     }
+    for (; s < steps; ++s) step(s, s & 1u);
 
     // result register r of a lane: row 8 (r/4) + 4 half + r%4, column lane mod 32;
     // positions of the last group stand for the row's last eight columns
