@@ -81,7 +81,7 @@ template <> struct Offset<true> { using T = uint64_t; };
 template <typename T, typename O>
 __device__ __forceinline__ const GLOBAL_AS T *at_offset(const T *base, O bytes) {
     auto *b = (const GLOBAL_AS char *)(base);
-    if constexpr (sizeof(O) == 4) asm volatile("" : "+s"(b));
+    if constexpr (sizeof(O) == 4) asm("" : "+s"(b));
     return (const GLOBAL_AS T *)(b + bytes);
 }
 
