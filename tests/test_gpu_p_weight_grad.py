@@ -35,7 +35,8 @@ def space(tokens, n_out, n_in):
 # tokens, n_out, n_in: single elements, ragged edges of tiles and steps, split tokens
 SHAPES = [(1, 1, 1), (1, 5, 33), (2, 64, 32), (63, 17, 100), (64, 128, 128), (65, 129, 127),
           (130, 256, 256), (200, 300, 520), (777, 96, 31), (1000, 130, 258), (2048, 64, 64),
-          (5000, 33, 40), (128, 4100, 4097), (70, 4096, 4224)]
+          (5000, 33, 40), (128, 4100, 4097), (70, 4096, 4224), (4096, 2000, 700),
+          (9001, 1030, 770), (12_345, 2304, 768), (300, 9, 8), (300, 8, 1000), (129, 2050, 7)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])

@@ -11,14 +11,15 @@
 //
 // LDS columns are permuted in units of 16 (32 B): unit u of token t sits at
 // u ^ 2 (t mod 4), so the four token rows that 16 lanes read at once, and the
-// next 16 lanes' rows, fall on different banks.
+// next 16 lanes' rows, fall on different banks (64-column tiles, whose rows are half
+// the banks: u ^ (t & 2)).  Measured bank conflicts: none.
 //
 // The loop keeps one step of global loads in registers and two steps in LDS:
 // step s multiplies buffer s mod 2 while step s+1 is written to the other and
 // step s+2 is on its way from memory, with one barrier a step.
 //
-// Few tiles: the tokens are split over `splits` blocks of a tile, which write
-// FP32 partial products; a second kernel adds them in split order.
+// Few tiles: the tokens are split over several blocks of a tile, which write FP32
+// partial products; a second kernel adds them in split order.
 #include "grad_device.h"
 
 #pragma clang fp contract(off)
@@ -34,7 +35,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr uint32_t kStep = 64;   // tokens a step of the loop
 
 template <int F>
 __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
@@ -113,7 +113,7 @@ enum class Out { k16, k32, kAdd32 };   // 16-bit result, FP32 result, added to F
 struct GradShape {
     uint64_t lddy;
     uint32_t tokens, n_out, n_in, blocks_in;   // blocks_in: exponent bytes a row
-    uint32_t per_split;                        // tokens a split (a multiple of kStep)
+    uint32_t per_split;                        // tokens a split (whole steps)
     uint32_t tiles_out, tiles_in;
     uint32_t group_i;                          // tiles a group has along n_in, 0: no groups
     uint64_t work;                             // work items: tiles, or places in groups
@@ -145,7 +145,7 @@ __device__ __forceinline__ bool tile_of(const GradShape &g, uint64_t w, uint32_t
 // other group holds.  Groups past the row's end read the same columns and store
 // nothing.  TINY (n_out or n_in below 8): element by element.  Tokens past the end
 // of the split are read as its last token and replaced by zeros.
-template <int F, Out O, int BM, int BN, int WM, int WN, bool TINY>
+template <int F, Out O, int BM, int BN, int WM, int WN, int kStep, bool TINY>
 __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     void *__restrict__ out, const uint16_t *__restrict__ dy, const uint8_t *__restrict__ q,
     const uint8_t *__restrict__ e, GradShape g) {
@@ -247,7 +247,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     };
     // LDS place of eight columns c of row r in a tile of `width` columns
     auto place = [](uint32_t r, uint32_t c, uint32_t width) {
-        return r * width + (((c >> 4) ^ ((r & 3u) << 1)) << 4) + (c & 15u);
+        const uint32_t turn = width >= 128 ? (r & 3u) << 1 : r & 2u;
+        return r * width + (((c >> 4) ^ turn) << 4) + (c & 15u);
     };
     auto stage_a = [&](uint32_t buf) {
 #pragma unroll
@@ -321,27 +322,25 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     // wave's LDS reads, conversions, LDS writes and requests are dealt between its MFMAs.
     constexpr int kMfma = TM * TN, kReads = 2 * (TM + TN);
     auto steady = [&](uint32_t s, uint32_t buf) {
-        static_assert(KK == 4, "the barrier stands before the last MFMA step");
-        read(1, buf, 1);
-        multiply(0);
-        stage_a(buf ^ 1u);
-        load_a(s + 2);
-        interleave<kMfma, kReads, 0, PA, PA>();
-        __builtin_amdgcn_sched_barrier(0);
-        read(0, buf, 2);
-        multiply(1);
-        stage_b(buf ^ 1u);
-        load_b(s + 2);
-        interleave<kMfma, kReads, 12 * PB, PB, 2 * PB>();
-        __builtin_amdgcn_sched_barrier(0);
-        read(1, buf, 3);
-        multiply(0);
-        interleave<kMfma, kReads, 0, 0, 0>();
-        __syncthreads();
-        read(0, buf ^ 1u, 0);
-        multiply(1);
-        interleave<kMfma, kReads, 0, 0, 0>();
-        __builtin_amdgcn_sched_barrier(0);
+        static_assert(KK >= 4 && KK % 2 == 0, "staging takes two MFMA steps, fragments alternate");
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            if (kk + 1 == KK) __syncthreads();
+            read((kk + 1) & 1, kk + 1 == KK ? buf ^ 1u : buf, (kk + 1) % KK);
+            multiply(kk & 1);
+            if (kk == 0) {
+                stage_a(buf ^ 1u);
+                load_a(s + 2);
+                interleave<kMfma, kReads, 0, PA, PA>();
+            } else if (kk == 1) {
+                stage_b(buf ^ 1u);
+                load_b(s + 2);
+                interleave<kMfma, kReads, 12 * PB, PB, 2 * PB>();
+            } else {
+                interleave<kMfma, kReads, 0, 0, 0>();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     auto step = [&](uint32_t s, uint32_t buf) {
         const bool more = s + 1 < steps;
@@ -438,26 +437,51 @@ uint32_t capped_blocks(uint64_t n) {
 // Tile and splits of a call, by its extents alone (so the workspace and the order
 // of the sums do not depend on the device).
 struct Plan {
-    bool big;          // 256 x 256 tiles, else 128 x 128
+    uint32_t tile;        // 256, 128 or 64 columns of each operand
     uint32_t splits;
     uint32_t per_split;
 };
 
 constexpr uint64_t kFill = 256;   // compute units of the chip
-constexpr uint64_t kMaxStride = 1ull << 24;   // kStep rows and a row's columns below 2^32 bytes
+constexpr uint64_t kMaxStride = 1ull << 24;   // a step's rows stay below 2^32 bytes
+constexpr uint64_t kSplitUnit = 128;          // tokens: whole steps of every tile
 
+// Measured on MI355X, one tile a compute unit, in ns: 64 tokens of a tile, and a
+// tile's start and end.  The large tile reuses each operand most but needs many tiles
+// and many tokens; a small one starts quickly and is bound by latency.
+struct TileCost {
+    uint32_t tile, step, ends;
+};
+constexpr TileCost kTiles[3] = {{256, 1900, 15000}, {128, 660, 4000}, {64, 310, 2000}};
+
+// The tile and splits of least estimated time: rounds of 256 tiles, and for split
+// tokens the join's launch, its partial products (about 8 TB/s out of the caches) and
+// its walk over the splits.  Over fourteen shapes of 200 to 16384 tokens and 64 to
+// 50257 columns the choice was within 12% of the best of every tile with 1 to 64
+// splits; for 16384 x 768 x 768, for example, 128 x 128 tiles in 6 splits take 44 us,
+// 64 x 64 in 3 53 us and 256 x 256 in 16 55 us, and for 1024 x 768 x 768 64 x 64
+// tiles 9 us, 128 x 128 17 us.
 Plan plan_of(uint64_t tokens, uint64_t n_out, uint64_t n_in) {
-    auto tiles = [&](uint64_t b) { return ((n_out + b - 1) / b) * ((n_in + b - 1) / b); };
-    Plan p;
-    p.big = tiles(256) >= kFill;
-    const uint64_t n = tiles(p.big ? 256 : 128);
-    const uint64_t steps = (tokens + kStep - 1) / kStep;
-    uint64_t s = 1;
-    while (n * s < kFill && steps / (s + 1) >= 8) ++s;
-    const uint64_t per = (steps + s - 1) / s;
-    p.splits = static_cast<uint32_t>((steps + per - 1) / per);
-    p.per_split = static_cast<uint32_t>(per * kStep);
-    return p;
+    const uint64_t units = (tokens + kSplitUnit - 1) / kSplitUnit;
+    const uint64_t plane_ns = n_out * n_in / 1000;          // 4 B written and read: 8 B a result
+    Plan best{0, 1, 0};
+    uint64_t best_ns = ~0ull;
+    for (const TileCost &c : kTiles) {
+        const uint64_t n = ((n_out + c.tile - 1) / c.tile) * ((n_in + c.tile - 1) / c.tile);
+        for (uint64_t s = 1; s <= 64 && s <= units && (s == 1 || n * s <= 2 * kFill); ++s) {
+            const uint64_t per = (units + s - 1) / s, used = (units + per - 1) / per;
+            if (used != s) continue;
+            const uint64_t rounds = (n * s + kFill - 1) / kFill;
+            uint64_t ns = rounds * (per * (kSplitUnit / 64) * c.step + c.ends);
+            if (s > 1) ns += 5000 + s * (plane_ns + 150);
+            if (ns < best_ns) {
+                best_ns = ns;
+                best = Plan{c.tile, static_cast<uint32_t>(s),
+                            static_cast<uint32_t>(per * kSplitUnit)};
+            }
+        }
+    }
+    return best;
 }
 
 template <int F, Out O>
@@ -465,12 +489,18 @@ hipError_t tiles_of(void *out, const uint16_t *dy, const uint8_t *q, const uint8
                     const GradShape &g, const Plan &p, bool tiny, hipStream_t stream) {
     const uint64_t cap = max_blocks();
     const dim3 grid(static_cast<uint32_t>(g.work < cap ? g.work : cap), p.splits);
+#define ZS_TILE(B, WM, WN, STEP, TINY)                                                    \
+    weight_grad_kernel<F, O, B, B, WM, WN, STEP, TINY>                                    \
+        <<<grid, 64 * WM * WN, 0, stream>>>(out, dy, q, e, g)
     if (tiny)
-        weight_grad_kernel<F, O, 128, 128, 2, 2, true><<<grid, 256, 0, stream>>>(out, dy, q, e, g);
-    else if (p.big)
-        weight_grad_kernel<F, O, 256, 256, 4, 2, false><<<grid, 512, 0, stream>>>(out, dy, q, e, g);
+        ZS_TILE(64, 2, 2, 64, true);
+    else if (p.tile == 256)
+        ZS_TILE(256, 4, 2, 64, false);
+    else if (p.tile == 128)
+        ZS_TILE(128, 2, 2, 64, false);
     else
-        weight_grad_kernel<F, O, 128, 128, 2, 2, false><<<grid, 256, 0, stream>>>(out, dy, q, e, g);
+        ZS_TILE(64, 2, 2, 128, false);
+#undef ZS_TILE
     return hipGetLastError();
 }
 
@@ -500,7 +530,7 @@ hipError_t launch_weight_grad(void *dw, bool dw32, bool first, const uint16_t *d
                               hipStream_t stream) {
     const Plan p = plan_of(tokens, n_out, n_in);
     const bool tiny = n_out < 8 || n_in < 8 || n_in >= kMaxStride || lddy >= kMaxStride;
-    const uint64_t b = p.big && !tiny ? 256 : 128;
+    const uint64_t b = tiny ? 64 : p.tile;
     const uint64_t tiles_in = (n_in + b - 1) / b, tiles_out = (n_out + b - 1) / b;
     GradShape g{lddy,
                 static_cast<uint32_t>(tokens),
