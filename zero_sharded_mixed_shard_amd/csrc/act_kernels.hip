@@ -47,65 +47,62 @@ struct Group {
     }
 };
 
-template <int F>
-__device__ __forceinline__ float exp_of(float x) {
-    if constexpr (F == 2)
-        return expf(x);
-    else
-        return exp_fast(x);   // its error is far below the 16-bit rounding's
-}
-
-template <int F>
-__device__ __forceinline__ float reciprocal(float d) {
-    if constexpr (F == 2)
-        return 1.0f / d;
-    else
-        return __builtin_amdgcn_rcpf(d);
-}
-
-// s(t) = 1 / (1 + e^-t)
-template <int F>
-__device__ __forceinline__ float logistic(float t) {
-    return reciprocal<F>(1.0f + exp_of<F>(-t));
-}
-
-// s(t) and s(-t) = e^-t s(t), neither by a difference.  e^-t is held at 2^125, where
-// s(t) is 2^-125 and s(-t) is 1 (the comparison keeps a NaN).
-template <int F>
-__device__ __forceinline__ void logistic_pair(float t, float *s, float *other) {
-    float x = exp_of<F>(-t);
-    x = x > 0x1p125f ? 0x1p125f : x;
-    *s = reciprocal<F>(1.0f + x);
-    *other = x * *s;
-}
-
+// Activation functions, act(x) = x s(t) with s(t) = 1 / (1 + e^-t).  FP32 data takes
+// the library's exponential and a division; for 16-bit data the constants are folded
+// into one polynomial, e^-t = 2^(x (a + b x^2)), and the hardware's 2^x and reciprocal
+// (each within an ulp) do, as the result is rounded to 16 bits.  The arithmetic is what
+// bounds the GELU kernels once the memory streams well: about twenty VALU operations
+// and two quarter-rate ones an element.
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// e^-t
+template <int F, int ACT>
+__device__ __forceinline__ float exp_neg_t(float x) {
+    if constexpr (F == 2) {
+        const float t =
+            ACT == ZERO_ACT_SILU ? x : 2.0f * kGeluC * (x + kGeluA * x * x * x);
+        return expf(-t);
+    } else if constexpr (ACT == ZERO_ACT_SILU) {
+        return __builtin_amdgcn_exp2f(x * -kLog2e);
+    } else {
+        constexpr float a = -2.0f * kGeluC * kLog2e, b = a * kGeluA;
+        return __builtin_amdgcn_exp2f(x * __builtin_fmaf(b, x * x, a));
+    }
+}
 
 template <int F, int ACT>
 __device__ __forceinline__ float act_value(float x) {
-    if constexpr (ACT == ZERO_ACT_SILU)
-        return x * logistic<F>(x);
-    else
-        return x * logistic<F>(2.0f * kGeluC * (x + kGeluA * x * x * x));
+    const float d = 1.0f + exp_neg_t<F, ACT>(x);
+    return F == 2 ? x * (1.0f / d) : x * __builtin_amdgcn_rcpf(d);
 }
 
-// act'(x) = s(t) + x s(t) s(-t) t'.  Past |x| = 20 the GELU's slope is 0 or
-// 1 in FP32; holding x there keeps the cube finite (comparisons keep a NaN).
+// act'(x) = s(t) + x s(t) s(-t) t' = s(t) (1 + x t' s(-t)).
+// Past |x| = 20 the GELU's slope is 0 or 1; t' is taken from x held there, which keeps
+// it finite.  A NaN gets through s(t).
+// FP32: s(-t) = e^-t s(t), without a difference, e^-t held at 2^125 where s(t) is
+// 2^-125 and s(-t) 1.  16-bit: 1 - s(t), whose error (2^-24, next to x t' of at most
+// some dozens where it matters) is far below the rounding to come.
 template <int F, int ACT>
 __device__ __forceinline__ float act_slope(float x) {
-    if constexpr (ACT == ZERO_ACT_SILU) {
-        float s, o;
-        logistic_pair<F>(x, &s, &o);
-        return s + x * s * o;
-    } else {
-        x = x > 20.0f ? 20.0f : x;
-        x = x < -20.0f ? -20.0f : x;
-        float s, o;
-        logistic_pair<F>(2.0f * kGeluC * (x + kGeluA * x * x * x), &s, &o);
-        const float dt = 2.0f * kGeluC * (1.0f + 3.0f * kGeluA * x * x);
-        return s + x * s * o * dt;
+    float xt = x;   // x t'
+    if constexpr (ACT == ZERO_ACT_GELU) {
+        constexpr float a = 2.0f * kGeluC, b = 3.0f * a * kGeluA;
+        const float h = __builtin_amdgcn_fmed3f(x, -20.0f, 20.0f);
+        xt = h * __builtin_fmaf(b, h * h, a);
     }
+    float s, o;
+    if constexpr (F == 2) {
+        float v = exp_neg_t<F, ACT>(x);
+        v = v > 0x1p125f ? 0x1p125f : v;   // a NaN stays
+        s = 1.0f / (1.0f + v);
+        o = v * s;
+    } else {
+        s = __builtin_amdgcn_rcpf(1.0f + exp_neg_t<F, ACT>(x));
+        o = 1.0f - s;
+    }
+    return s * __builtin_fmaf(xt, o, 1.0f);
 }
 
 // Maximum over the four lanes of a block (quad permutes 1,0,3,2 and 2,3,0,1).
@@ -116,18 +113,23 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t a) {
     return a > b ? a : b;
 }
 
-// Codes of eight values of a block whose exponent byte is eb.
-template <int F>
+// Codes of eight values of a block whose exponent byte is eb.  RARE: some value of
+// the wave is not finite or lies above the largest a checkpoint stands for.
+template <int F, bool RARE>
 __device__ __forceinline__ u32x2 encode8(const float x[8], uint32_t eb) {
     const float inv = from_bits((254u - eb) << 23);   // 2^-k
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const bool bad = (bits(x[j]) & 0x7fffffffu) >= 0x7f800000u;
         float c = x[j];
-        c = c > kTop<F> ? kTop<F> : c;
-        c = c < -kTop<F> ? -kTop<F> : c;
-        v[j] = bad ? from_bits(0x7fc00000u) : c * inv;
+        if constexpr (RARE) {
+            c = c > kTop<F> ? kTop<F> : c;
+            c = c < -kTop<F> ? -kTop<F> : c;
+            const bool bad = (bits(x[j]) & 0x7fffffffu) >= 0x7f800000u;
+            v[j] = bad ? from_bits(0x7fc00000u) : c * inv;
+        } else {
+            v[j] = c * inv;
+        }
     }
     u32x2 r;
 #pragma unroll
@@ -137,6 +139,17 @@ __device__ __forceinline__ u32x2 encode8(const float x[8], uint32_t eb) {
             __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], w, true));
     }
     return r;
+}
+
+// Largest magnitude of eight values as FP32 bits; a NaN or infinity counts as such.
+__device__ __forceinline__ uint32_t magnitude8(const float x[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t a = bits(x[j]) & 0x7fffffffu;
+        m = a > m ? a : m;
+    }
+    return m;
 }
 
 // The values eight codes stand for: code * 2^(eb - 127), exact in FP32.
@@ -197,16 +210,20 @@ __global__ __launch_bounds__(kThreads) void act_save_kernel(
             const uint64_t g = t0 + u * kThreads + threadIdx.x;
             if (g < n_groups) {   // n_groups is a multiple of 4: whole blocks take part
                 const Group<FLAT> p(g, nb, cols);
-                uint32_t m = 0;
+                uint32_t m = magnitude8(v[u]);
+                const bool rare = __any(m > bits(kTop<F>));
+                if (rare) {   // the block's scale goes by its finite elements
+                    m = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t a = bits(v[u][j]) & 0x7fffffffu;
-                    m = a < 0x7f800000u && a > m ? a : m;
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t a = bits(v[u][j]) & 0x7fffffffu;
+                        m = a < 0x7f800000u && a > m ? a : m;
+                    }
                 }
                 m = quad_max(m);
                 const int b0 = static_cast<int>(m >> 23) - 8 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
                 const uint32_t eb = static_cast<uint32_t>(b0 < 3 ? 3 : b0);
-                const u32x2 c = encode8<F>(v[u], eb);
+                const u32x2 c = rare ? encode8<F, true>(v[u], eb) : encode8<F, false>(v[u], eb);
                 store_codes(q + p.row * cols + p.col, p.n, c);
                 if ((g & 3) == 0) e[g >> 2] = static_cast<uint8_t>(eb);
                 if constexpr (ACT != ZERO_ACT_NONE) {
