@@ -31,7 +31,7 @@ constexpr float kInf = __builtin_inff();
 
 template <int F> constexpr int kPer = F == 2 ? 4 : 8;   // logits of a 16-B vector
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 // e^(z - m), c = m log2 e.
 __device__ __forceinline__ float exp_from(float z, float c) {
@@ -185,14 +185,48 @@ __device__ __forceinline__ float exp_minus_1(float d) {
     for (int n = 12; n >= 2; --n) s = __builtin_fmaf(d * (1.0f / n), s, 1.0f);
     return d * s;
 }
+__device__ __forceinline__ float exp_of(float x) {
+    return __builtin_fabsf(x) <= 1.0f ? 1.0f + exp_minus_1(x) : exp_fast(x);
+}
 
-// The row's loss from c = max log2 e and the sum; lane 0 writes token_loss and logp.
-__device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, float c, float sum,
-                                              float z_target, float w, uint32_t lane) {
-    const float logp =
-        (__builtin_fmaf(z_target, kLog2e, -c) - __builtin_amdgcn_logf(sum)) * kLn2;   // log2
+// ln(x) for x of normal FP32 range, to about 2^-25 absolute next to the exact multiple
+// of ln 2: x = 2^k f, f in [0.7, 1.42), ln f = 2 atanh((f - 1) / (f + 1)) by its series
+// (the first term left out is below 2^-30).  Anything else as the hardware's logarithm
+// has it (0, infinity, NaN).
+__device__ __forceinline__ double log_of(float x) {
+    if (!(x >= 0x1p-126f && x < kInf))
+        return static_cast<double>(__builtin_amdgcn_logf(x));
+    int k = __builtin_amdgcn_frexp_expf(x);
+    float f = __builtin_amdgcn_frexp_mantf(x);     // [0.5, 1)
+    if (f < 0.70710678f) {
+        f = f + f;
+        k = k - 1;
+    }
+    const float q = (f - 1.0f) / (f + 1.0f), q2 = q * q;
+    float p = 1.0f / 11.0f;
+    p = __builtin_fmaf(p, q2, 1.0f / 9.0f);
+    p = __builtin_fmaf(p, q2, 1.0f / 7.0f);
+    p = __builtin_fmaf(p, q2, 1.0f / 5.0f);
+    p = __builtin_fmaf(p, q2, 1.0f / 3.0f);
+    const float ln_f = 2.0f * __builtin_fmaf(q * q2, p, q);
+    return static_cast<double>(k) * 0.693147180559945309417 + static_cast<double>(ln_f);
+}
+
+// The row's loss from its maximum m, c = m log2 e as rounded, and the sum of
+// 2^(z log2 e - c); lane 0 writes token_loss and logp.  Losses of both signs cancel in
+// the total, so the log-probability and its distances to the old and the reference one
+// are taken in FP64: c's rounding, m log2 e - c, is known exactly from one fused
+// operation, and what is left is the sum's own error.
+__device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, float m, float c,
+                                              float sum, float z_target, float w, uint32_t lane) {
+    const double rest = static_cast<double>(__builtin_fmaf(m, kLog2e, -c)) * 0.693147180559945309417;
+    const double lp = (static_cast<double>(z_target) - static_cast<double>(m)) -
+                      (log_of(sum) - rest);
+    const float logp = static_cast<float>(lp);
     const float A = a.advantage[t];
-    const float r = a.old_logp != nullptr ? exp_fast(logp - a.old_logp[t]) : 1.0f;
+    float r = 1.0f;
+    if (a.old_logp != nullptr)
+        r = exp_of(static_cast<float>(lp - static_cast<double>(a.old_logp[t])));
     const float lo = 1.0f - a.clip_low, hi = 1.0f + a.clip_high;
     float rc = r < lo ? lo : r;
     rc = rc > hi ? hi : rc;
@@ -201,7 +235,8 @@ __device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, f
     const bool cut = (A > 0.0f && r > hi) || (A < 0.0f && r < lo);
     float g = cut ? 0.0f : p0;
     if (a.ref_logp != nullptr && a.kl_coef != 0.0f) {
-        const float d = a.ref_logp[t] - logp, em = exp_minus_1(d);
+        const float d = static_cast<float>(static_cast<double>(a.ref_logp[t]) - lp);
+        const float em = exp_minus_1(d);
         L = L + a.kl_coef * (em - d);
         g = g - a.kl_coef * em;
     }
@@ -346,7 +381,7 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
         const float ze = r.edge != ~0u ? to_f32<F>(row[r.edge]) : -kInf;
 #pragma unroll
         for (int i = 0; i < N; ++i) take(x[i]);
-        const float c = block_reduce<T, true>(max_nan(most.value(), ze), red) * kLog2e;
+        const float m = block_reduce<T, true>(max_nan(most.value(), ze), red), c = m * kLog2e;
         float s = exp_from(ze, c);
         auto add = [&](const u32x4 &w) {
             float z[kPer<F>];
@@ -366,7 +401,7 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
             add(held[i][lane]);
         }
         s = block_reduce<T, false>(s, red);
-        const RowGrad g = finish_row(a, t, c, s, zt, weight, lane);
+        const RowGrad g = finish_row(a, t, m, c, s, zt, weight, lane);
         auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
         asm volatile("" : "+s"(n_vec));
 #pragma unroll
@@ -426,7 +461,7 @@ __global__ __launch_bounds__(kBlock<T>) void policy_long_kernel(PolicyArgs a) {
         s = block_reduce<T, false>(
             m == -kInf ? s : s * __builtin_amdgcn_exp2f(c - rc), red);
         if (rm == -kInf) s = __builtin_nanf("");   // nothing left to choose from
-        const RowGrad g = finish_row(a, t, rc, s, zt, weight, lane);
+        const RowGrad g = finish_row(a, t, rm, rc, s, zt, weight, lane);
         if (a.dlogits == nullptr) continue;
         auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
         for (uint32_t j = 0; j + lane < r.n_vec; j += T)
