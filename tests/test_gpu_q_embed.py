@@ -34,7 +34,8 @@ def ids_of(tokens, vocab, seed, kind="mixed", dtype=torch.int64):
 @pytest.mark.parametrize("itype", [torch.int32, torch.int64])
 @pytest.mark.parametrize("tokens,vocab,width,gap,scale", [
     (1, 1, 1, 0, 1.0), (1, 100, 768, 0, 1.0), (7, 50, 33, 0, 0.5), (130, 1000, 64, 8, 27.7),
-    (1000, 77, 255, 1, -1.3), (3, 5, 8192, 0, 1.0), (513, 300, 7, 2, 2.0)])
+    (1000, 77, 255, 1, -1.3), (3, 5, 8192, 0, 1.0), (513, 300, 7, 2, 2.0),
+    (37, 90, 2051, 3, 0.3), (5, 9, 4099, 0, 3.0), (200, 40, 513, 1, 1.0), (11, 6, 259, 0, 1.7)])
 def test_lookup_is_exact(tokens, vocab, width, gap, scale, itype, dt):
     g = torch.Generator().manual_seed(width)
     h = torch.randn(vocab, width, generator=g).to(plain.TORCH[dt])
