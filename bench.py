@@ -482,6 +482,79 @@ def measure_extras(dev, n_elem: int = 1 << 30, reps: int = 5) -> dict:
     return out
 
 
+def measure_gradient_operators(dev, reps: int = 5) -> dict:
+    """The operators that make a rank's gradients (HIP events), on a 16384-token
+    micro-batch of a wide layer: algorithmic GB/s, and TFLOP/s of the weight gradient."""
+    import torch
+
+    import synth
+    import zero_sharded_mixed_shard_amd as zs
+
+    out = {}
+    stream = torch.cuda.current_stream(dev)
+    bf16 = torch.bfloat16
+
+    def record(name, nbytes, fn, flops=None):
+        fn()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record(stream)
+        for _ in range(reps):
+            fn()
+        e1.record(stream)
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / reps
+        gbps = nbytes / (ms * 1e-3) / 1e9
+        out[name] = {"ms": ms, "GBps": gbps, "frac": gbps / PEAK_HBM_GBPS}
+        if flops is not None:
+            out[name]["TFLOPs"] = flops / (ms * 1e-3) / 1e12
+
+    def normal(rows, cols, std, seed):
+        flat = torch.empty(rows * cols, dtype=bf16, device=dev)
+        return synth.fill_normal_(flat, std, seed).view(rows, cols)
+
+    tokens, width, hidden, vocab = 16384, 4096, 8192, 50257
+    x = normal(tokens, hidden, 1.0, 31)
+    y = torch.empty_like(x)
+    q = torch.empty(tokens, hidden, dtype=torch.uint8, device=dev)
+    e = torch.empty(tokens, hidden // zs.ACT_BLOCK, dtype=torch.uint8, device=dev)
+    n, held = x.numel(), q.numel() + e.numel()
+    record("act_save", 2 * n + held, lambda: zs.zero_act_save(q, e, x))
+    record("act_load", 2 * n + held, lambda: zs.zero_act_load(y, q, e))
+    record("act_save_gelu", 4 * n + held,
+           lambda: zs.zero_act_save(q, e, x, act=zs.ACT_GELU, y=y))
+    record("act_backward_gelu", 4 * n + held,
+           lambda: zs.zero_act_backward(y, x, q, e, zs.ACT_GELU))
+    dy = normal(tokens, width, 1e-2, 32)
+    dw = torch.empty(width, hidden, dtype=bf16, device=dev)
+    ws = torch.empty(zs.zero_weight_grad_workspace(tokens, width, hidden), dtype=torch.uint8,
+                     device=dev)
+    record("weight_grad", 2 * dy.numel() + held + 2 * dw.numel(),
+           lambda: zs.zero_weight_grad(dw, dy, q, e, workspace=ws), 2 * tokens * width * hidden)
+    del x, y, q, e, dw, ws
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(33)
+    ids = torch.randint(0, vocab, (tokens,), generator=gen, device=dev)
+    table = normal(vocab, width, 0.02, 34)
+    rows = torch.empty(tokens, width, dtype=bf16, device=dev)
+    record("embed_lookup", 4 * rows.numel(), lambda: zs.zero_embed_lookup(rows, table, ids))
+    grad = torch.empty(vocab, width, dtype=bf16, device=dev)
+    ws = torch.empty(zs.zero_embed_grad_workspace(tokens, vocab, width), dtype=torch.uint8,
+                     device=dev)
+    record("embed_grad", 2 * dy.numel() + 2 * grad.numel(),
+           lambda: zs.zero_embed_grad(grad, dy, ids, workspace=ws))
+    del table, rows, grad, ws, dy
+    logits = normal(tokens, vocab, 2.0, 35)
+    dlogits = torch.empty_like(logits)
+    per_row = [torch.full((tokens,), v, device=dev) for v in (0.0, 0.0, 1.0, 1.0 / tokens, -11.0)]
+    token, logp, advantage, weight, before = per_row
+    loss = torch.empty(1, device=dev)
+    record("policy_loss", 4 * logits.numel(), lambda: zs.zero_policy_loss(
+        loss, token, logp, logits, ids, advantage, weight, old_logp=before, ref_logp=before,
+        clip_low=0.2, clip_high=0.2, kl_coef=0.05, loss_scale=1.0, dlogits=dlogits))
+    return out
+
+
 def measure_small(dev, steps: int = 300, warmup: int = 20) -> dict:
     """Whole-step time of the launch-bound workloads under three kinds of control.
 
@@ -638,7 +711,8 @@ def main():
                     help="timed steps of each configuration under 'workloads'")
     ap.add_argument("--extras", action="store_true",
                     help="also time the accumulate / FP32-gradient / device-control / exchange "
-                         "kernels on shards of --extras-elems elements (reported under 'extras')")
+                         "kernels on shards of --extras-elems elements and the gradient operators "
+                         "(reported under 'extras')")
     ap.add_argument("--extras-elems", type=int, default=1 << 30,
                     help="shard size of the --extras measurements (elements)")
     ap.add_argument("--small", action="store_true",
@@ -784,6 +858,7 @@ def main():
     if args.extras:
         log("[bench] extras ...")
         extras = measure_extras(dev, n_elem=args.extras_elems)
+        extras["gradient_operators"] = measure_gradient_operators(dev)
 
     out = {
         "metric": METRIC,
