@@ -205,6 +205,8 @@ constexpr int kSortThreads = 256;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr uint32_t kSortMin = 1024;           // tokens a sort block takes at least
 
+constexpr uint32_t kBatch = 4;                // 64-token steps whose keys are in flight
+
 // Lanes of the wave whose digit equals this lane's, among the active ones.
 __device__ __forceinline__ uint64_t peers_of(uint32_t digit, bool on) {
     uint64_t m = __ballot(on);
@@ -230,8 +232,18 @@ __device__ __forceinline__ void wave_histogram(uint32_t (*cnt)[kDigits], uint32_
     const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     for (uint32_t d = lane; d < kDigits; d += 64) cnt[wave][d] = 0;
     wave_sync();
-    for (uint32_t t = first + lane; t < last; t += 64)
-        atomicAdd(&cnt[wave][(key_of(t) >> shift) & (kDigits - 1)], 1u);
+    for (uint32_t t0 = first; t0 < last; t0 += 64 * kBatch) {
+        uint32_t k[kBatch];
+#pragma unroll
+        for (uint32_t i = 0; i < kBatch; ++i) {
+            const uint32_t t = t0 + i * 64 + lane;
+            k[i] = t < last ? key_of(t) : 0u;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kBatch; ++i)
+            if (t0 + i * 64 + lane < last)
+                atomicAdd(&cnt[wave][(k[i] >> shift) & (kDigits - 1)], 1u);
+    }
 }
 
 // The first pass reads ids (keys_in null); later passes read keys and order.
@@ -277,14 +289,23 @@ __global__ __launch_bounds__(kSortThreads) void radix_scatter_kernel(
     // a digit's tokens over all blocks, and over the blocks before this one
     constexpr uint32_t kMine = kDigits / kSortThreads;
     uint32_t before[kMine] = {}, all[kMine] = {};
-#pragma unroll 8
-    for (uint32_t b = 0; b < gridDim.x; ++b) {
+    constexpr uint32_t kFlight = 32;   // blocks whose counts are in flight
+    for (uint32_t b0 = 0; b0 < gridDim.x; b0 += kFlight) {
+        uint32_t h[kFlight][kMine];
 #pragma unroll
-        for (uint32_t i = 0; i < kMine; ++i) {
-            const uint32_t h = hist[b * kDigits + threadIdx.x + i * kSortThreads];
-            all[i] += h;
-            before[i] += b < blockIdx.x ? h : 0u;
-        }
+        for (uint32_t b = 0; b < kFlight; ++b)
+#pragma unroll
+            for (uint32_t i = 0; i < kMine; ++i)
+                h[b][i] = b0 + b < gridDim.x
+                              ? hist[(b0 + b) * kDigits + threadIdx.x + i * kSortThreads]
+                              : 0u;
+#pragma unroll
+        for (uint32_t b = 0; b < kFlight; ++b)
+#pragma unroll
+            for (uint32_t i = 0; i < kMine; ++i) {
+                all[i] += h[b][i];
+                before[i] += b0 + b < blockIdx.x ? h[b][i] : 0u;
+            }
     }
 #pragma unroll
     for (uint32_t i = 0; i < kMine; ++i) total[threadIdx.x + i * kSortThreads] = all[i];
@@ -325,21 +346,30 @@ __global__ __launch_bounds__(kSortThreads) void radix_scatter_kernel(
         }
     }
     __syncthreads();
-    for (uint32_t t0 = first; t0 < last; t0 += 64) {
-        const uint32_t t = t0 + lane;
-        const bool on = t < last;
-        const uint32_t key = on ? key_of(t) : 0u;
-        const uint32_t digit = (key >> shift) & (kDigits - 1);
-        const uint64_t m = peers_of(digit, on);
-        const uint64_t lower = m & ((1ull << lane) - 1);
-        uint32_t place = 0;
-        if (on) place = cnt[wave][digit] + static_cast<uint32_t>(__popcll(lower));
-        wave_sync();
-        if (on && lower == 0) cnt[wave][digit] += static_cast<uint32_t>(__popcll(m));
-        wave_sync();
-        if (on) {
-            keys_out[place] = key;
-            order_out[place] = order_in != nullptr ? order_in[t] : t;
+    for (uint32_t b0 = first; b0 < last; b0 += 64 * kBatch) {
+        uint32_t keys[kBatch], orders[kBatch];
+#pragma unroll
+        for (uint32_t i = 0; i < kBatch; ++i) {
+            const uint32_t t = b0 + i * 64 + lane;
+            keys[i] = t < last ? key_of(t) : 0u;
+            orders[i] = t < last && order_in != nullptr ? order_in[t] : t;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kBatch; ++i) {
+            if (b0 + i * 64 >= last) break;
+            const bool on = b0 + i * 64 + lane < last;
+            const uint32_t digit = (keys[i] >> shift) & (kDigits - 1);
+            const uint64_t m = peers_of(digit, on);
+            const uint64_t lower = m & ((1ull << lane) - 1);
+            uint32_t place = 0;
+            if (on) place = cnt[wave][digit] + static_cast<uint32_t>(__popcll(lower));
+            wave_sync();
+            if (on && lower == 0) cnt[wave][digit] += static_cast<uint32_t>(__popcll(m));
+            wave_sync();
+            if (on) {
+                keys_out[place] = keys[i];
+                order_out[place] = orders[i];
+            }
         }
     }
 }
@@ -422,7 +452,7 @@ __device__ __forceinline__ void sum_chunk(elem_t<O> *dw, const RowSums &a, uint3
     uint32_t after = __shfl_down(key, 1);
     if (lane == kChunk - 1) after = next;
     const uint64_t ends = __ballot(after != key);   // last positions of their runs
-    bool from_before = __builtin_amdgcn_readfirstlane(key) == prev;
+    bool from_before = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(key)) == prev;
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (uint32_t i0 = 0; i0 < count; i0 += U) {
         Raw8<F> r[U];
@@ -449,7 +479,7 @@ __device__ __forceinline__ void sum_chunk(elem_t<O> *dw, const RowSums &a, uint3
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] += x[j];
             const bool end = (ends >> i) & 1u;
-            if (end || i == kChunk - 1) {
+            if (end || i + 1 == kChunk) {
                 if (n != 0) {
                     if (from_before)
                         store_part(part_row(a, c, 0, col), acc);
