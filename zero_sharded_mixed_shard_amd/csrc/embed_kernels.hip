@@ -586,10 +586,10 @@ __global__ __launch_bounds__(kSumThreads) void chunk_sum_kernel(
 }
 
 // acc[0..4) += parts [p0, p1) of the run that starts in chunk c: slot 1 of that chunk,
-// slot 0 of the following ones, in order, eight in flight.
+// slot 0 of the following ones, in order, U in flight.
+template <uint32_t U>
 __device__ __forceinline__ void add_parts(float acc[4], const RowSums &a, uint32_t c, uint32_t p0,
                                           uint32_t p1, uint32_t col) {
-    constexpr uint32_t U = 8;
     for (uint32_t p = p0; p < p1; p += U) {
         f32x4 x[U];
 #pragma unroll
@@ -600,9 +600,9 @@ __device__ __forceinline__ void add_parts(float acc[4], const RowSums &a, uint32
         }
 #pragma unroll
         for (uint32_t u = 0; u < U; ++u) {
-            if (p + u >= p1) break;
+            const bool on = p + u < p1;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] += x[u][j];
+            for (int j = 0; j < 4; ++j) acc[j] = on ? acc[j] + x[u][j] : acc[j];
         }
     }
 }
@@ -646,17 +646,17 @@ __global__ __launch_bounds__(kJoinThreads) void join_runs_kernel(elem_t<O> *__re
         for (uint64_t m = owners; m != 0; m &= m - 1) {
             const uint32_t l = static_cast<uint32_t>(__builtin_ctzll(m)), c = c0 + l;
             const uint32_t key = static_cast<uint32_t>(__builtin_amdgcn_readlane(own, l));
-            // parts of the run, as far as kShortRun tells
-            const uint64_t far = (static_cast<uint64_t>(c) + kShortRun) * chunk;
-            if (far < a.tokens && a.keys[far] == key) {
+            // the run reaches into a chunk whose first key is its own
+            const uint64_t at = (static_cast<uint64_t>(c) + 1 + lane) * chunk;
+            const uint64_t in = __ballot(lane < kShortRun && at < a.tokens && a.keys[at] == key);
+            if (in >> (kShortRun - 1)) {
                 longer |= 1ull << l;
                 continue;
             }
             if (turn++ % kJoinWaves != wave) continue;
-            const uint32_t n_part =
-                (wave_lower_bound(a.keys, a.tokens, key + 1) - 1) / chunk - c + 1;
+            const uint32_t n_part = 1 + static_cast<uint32_t>(__popcll(in));
             float acc[4] = {0, 0, 0, 0};
-            if (n != 0) add_parts(acc, a, c, 0, n_part, col);
+            if (n != 0) add_parts<4>(acc, a, c, 0, n_part, col);
             finish(key, acc);
         }
         for (uint64_t m = longer; m != 0; m &= m - 1) {
@@ -668,7 +668,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_runs_kernel(elem_t<O> *__re
                 return static_cast<uint32_t>(static_cast<uint64_t>(n_part) * w / kJoinWaves);
             };
             float acc[4] = {0, 0, 0, 0};
-            if (n != 0) add_parts(acc, a, c, share(wave), share(wave + 1), col);
+            if (n != 0) add_parts<16>(acc, a, c, share(wave), share(wave + 1), col);
             *reinterpret_cast<f32x4 *>(&sums[wave][lane * 4]) =
                 f32x4{acc[0], acc[1], acc[2], acc[3]};
             __syncthreads();

@@ -330,6 +330,9 @@ __device__ __forceinline__ uint64_t row_stride() {
 
 // One row a group of T lanes (a block, or one of the waves of a block), its logits on
 // chip: N vectors a lane in registers and L in LDS.
+// Four waves a SIMD leave 128 registers a lane.  The longest rows spill some 30 of them
+// around the row's scalar part; three waves a SIMD with more vectors a lane (384 lanes x
+// (31 + 12)) measured a third slower, as the arithmetic then hides less.
 template <int F, int T, int N, int L>
 __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) {
     constexpr int B = 3;                  // vectors on their way to LDS at once
