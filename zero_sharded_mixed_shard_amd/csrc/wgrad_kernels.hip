@@ -122,7 +122,7 @@ struct GradShape {
 // Tile of work item w: tiles in groups of `group_o` x `group_i` (32), groups dealt to
 // the eight XCDs in turn (workgroups go round them by number), so that the 32 compute
 // units of an XCD share operands in its L2 (4 x 8 tiles 943 us, 8 x 4 952 us, ungrouped
-// 1003 us at 16384 x 8192 x 4096).  false: no such tile.
+// 1003 us at 16384 x 8192 x 4096, same clock).  false: no such tile.
 __device__ __forceinline__ bool tile_of(const GradShape &g, uint64_t w, uint32_t *o, uint32_t *i) {
     if (g.group_i == 0) {
         *o = static_cast<uint32_t>(w / g.tiles_in);
@@ -155,11 +155,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     constexpr int kRowsA = kThreads * 8 / BM, kRowsB = kThreads * 8 / BN;  // rows a pass
     constexpr int PA = kStep / kRowsA, PB = kStep / kRowsB;                // passes a step
     constexpr int KK = kStep / 16;                                         // MFMA steps a step
+    // two buffers of each tile; arrays of their own, so that the compiler may move reads of
+    // one over writes of the other (one array for both: 3% slower)
     __shared__ __align__(16) uint16_t sa[2][kStep * BM];
     __shared__ __align__(16) uint16_t sb[2][kStep * BN];
 
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     for (uint64_t work = blockIdx.x; work < g.work; work += gridDim.x) {
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     uint32_t tile_o, tile_i;
     if (!tile_of(g, work, &tile_o, &tile_i)) continue;
     const uint32_t o0 = tile_o * BM, i0 = tile_i * BN;
@@ -369,6 +371,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     }
     for (; s < steps; ++s) step(s, s & 1u);
 
+    // the lane again, opaque: what the stores need is worked out here and not kept in
+    // registers (or spilled) from before the loop
+    uint32_t el = lane;
+    asm volatile("" : "+v"(el));
+    const uint32_t eh = el >> 5;
     // result register r of a lane: row 8 (r/4) + 4 half + r%4, column lane mod 32;
     // positions of the last group stand for the row's last eight columns
     auto column = [](uint32_t at, uint32_t first, uint32_t n) {   // ~0: not this one's to store
@@ -379,16 +386,56 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
         const uint32_t real = n - 8 + (c & 7u);
         return real >= group ? real : ~0u;
     };
+    if constexpr (O == Out::k16 && !TINY) {
+        // Stored as they lie, a wave's 16-bit results are 64-B pieces of 128-B lines (1.8
+        // times the bytes moved, a tenth of the time at 2048 tokens).  Each wave turns 32
+        // rows at a time through LDS (its own part: every wave is past the last barrier,
+        // behind which nothing is read) into rows of 16-B groups.  Units of 32 columns are
+        // swapped in every second four rows, so that the two halves of a wave write
+        // different banks.
+        constexpr uint32_t W = BN / WN, kPerRow = W / 8, kRows = 64 / kPerRow;
+        constexpr uint32_t kSwap = W >= 64 ? 32 : 0;
+        static_assert(WM * WN * 32 * W <= 2 * kStep * BM, "room for 32 rows a wave");
+        uint16_t *const mine = &sa[0][0] + wave * (32 * W);
+        const uint32_t c = el % kPerRow * 8, group = i0 + bn + c;
+#pragma unroll
+        for (int m = 0; m < TM; ++m) {
+#pragma unroll
+            for (int n = 0; n < TN; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    mine[(8 * (r / 4) + 4 * eh + r % 4) * W +
+                         ((n * 32 + (el & 31u)) ^ (eh * kSwap))] = from_f32<F>(acc[m][n][r]);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            for (uint32_t r0 = 0; r0 < 32; r0 += kRows) {
+                const uint32_t r = r0 + el / kPerRow;
+                const uint32_t row = column(am + m * 32 + r, o0, g.n_out);
+                if (row == ~0u || group >= g.n_in) continue;
+                const uint16_t *v = &mine[r * W + (c ^ (((r >> 2) & 1u) * kSwap))];
+                uint16_t *d = static_cast<uint16_t *>(out) + static_cast<uint64_t>(row) * g.n_in;
+                if (group + 8 <= g.n_in) {
+                    *reinterpret_cast<u32x4_any *>(d + group) = *reinterpret_cast<const u32x4 *>(v);
+                } else {   // the row's last eight columns, those from `group` on
+                    for (uint32_t k = group - (g.n_in - 8); k < 8; ++k) d[g.n_in - 8 + k] = v[k];
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+        __syncthreads();   // the next tile writes LDS
+        continue;
+    }
     const uint64_t plane = static_cast<uint64_t>(g.n_out) * g.n_in;
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
-        const uint32_t col = column(bn + n * 32 + (lane & 31u), i0, g.n_in);
+        const uint32_t col = column(bn + n * 32 + (el & 31u), i0, g.n_in);
 #pragma unroll
         for (int m = 0; m < TM; ++m) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 __builtin_amdgcn_sched_barrier(0);
-                const uint32_t row = column(am + m * 32 + 8 * (r / 4) + 4 * half + r % 4, o0,
+                const uint32_t row = column(am + m * 32 + 8 * (r / 4) + 4 * eh + r % 4, o0,
                                             g.n_out);
                 if (row != ~0u && col != ~0u) {
                     const uint64_t at = static_cast<uint64_t>(row) * g.n_in + col;
