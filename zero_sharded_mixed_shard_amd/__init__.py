@@ -49,6 +49,22 @@ Device-resident control (no read-back between steps):
     zero_overflow_check_dev(g16, psi, n, rank, ctl)
     zero_scaler_update_dev(ctl, bias, t_first)
     zero_adam_step_dev(w16, g16, master, m, v, psi, n, rank, lr=..., ..., ctl=ctl)
+
+The operators that make the gradients (include/zero_shard_grad.h; 2-D tensors with unit
+column stride, gradients at any offset of a flat buffer):
+
+    zero_act_save(q, e, x, act=ACT_NONE, y=None)       # 8-bit checkpoint of x, and y = act(x)
+    zero_act_load(x, q, e)                             # the values it stands for
+    zero_act_backward(dx, dy, q, e, act)               # dx = dy * act'(values)
+    zero_weight_grad(dw, dy, q, e, first=True, workspace=ws)       # dw = dy^T values
+    zero_weight_grad_workspace(tokens, n_out, n_in) -> bytes
+    zero_embed_lookup(out, table, ids, scale=1.0)
+    zero_embed_grad(dw, dy, ids, scale=1.0, first=True, workspace=ws)
+    zero_embed_grad_workspace(tokens, vocab, width) -> bytes
+    zero_policy_loss(loss, token_loss, logp, logits, targets, advantage, weight, *,
+                     old_logp=None, ref_logp=None, clip_low, clip_high, kl_coef, loss_scale,
+                     dlogits=None)
+    zero_policy_loss_dev(..., ctl=ctl)                 # loss scale from the control block
 """
 from ._binding import (  # noqa: F401
     LIB_PATH,
