@@ -172,3 +172,50 @@ def test_gradient_against_differences():
         up[o, i] += 0.5
         dn[o, i] -= 0.5
         assert abs(loss(up) - loss(dn) - float(dw[o, i])) <= bound[o, i] + 1e-10
+
+
+def test_row_strides_past_the_offsets_range():
+    # rows 2^24 + 16 elements apart (2.2 GB): the element-by-element form takes over
+    ld, tokens = (1 << 24) + 16, 70
+    buf = torch.zeros(ld * tokens, dtype=torch.bfloat16, device=DEV)
+    dy = buf.as_strided((tokens, 40), (ld, 1))
+    hdy, hx = whole(tokens, 40, 1), whole(tokens, 100, 2)
+    dy.copy_(hdy)
+    q, e = checkpoint(hx, "bf16")
+    dw = Framed(40, 100, torch.float32)
+    zs.zero_weight_grad(dw.t, dy, q, e, workspace=space(tokens, 40, 100))
+    assert torch.equal(dw.t.cpu().double(), hdy.double().t() @ hx.double()) and dw.intact()
+
+
+def test_a_checkpoint_wider_than_the_offsets_range():
+    n_in, tokens, n_out = (1 << 24) + 37, 3, 9
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    x = torch.randint(-4, 5, (tokens, n_in), generator=g, device=DEV).bfloat16()
+    q = torch.empty(tokens, n_in, dtype=torch.uint8, device=DEV)
+    e = torch.empty(tokens, -(-n_in // 32), dtype=torch.uint8, device=DEV)
+    zs.zero_act_save(q, e, x)
+    dy = whole(tokens, n_out, 3).bfloat16().to(DEV)
+    dw = torch.empty(n_out, n_in, device=DEV)
+    zs.zero_weight_grad(dw, dy, q, e, workspace=space(tokens, n_out, n_in))
+    want = sum(dy[t].float()[:, None] * x[t].float()[None, :] for t in range(tokens))
+    assert torch.equal(dw, want)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gradients_past_4_gib(dt):
+    # dw of 5.2 GB of FP32: offsets past 2^32 in its last rows
+    td = plain.TORCH[dt]
+    n_out, n_in, tokens = 40_003, 32_800, 5
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    dy = torch.randint(-4, 5, (tokens, n_out), generator=g, device=DEV).to(td)
+    x = torch.randint(-4, 5, (tokens, n_in), generator=g, device=DEV).to(td)
+    q = torch.empty(tokens, n_in, dtype=torch.uint8, device=DEV)
+    e = torch.empty(tokens, -(-n_in // 32), dtype=torch.uint8, device=DEV)
+    zs.zero_act_save(q, e, x)
+    dw = torch.empty(n_out, n_in, device=DEV)
+    zs.zero_weight_grad(dw, dy, q, e, workspace=space(tokens, n_out, n_in))
+    for r in (slice(0, 300), slice(n_out // 2, n_out // 2 + 300), slice(n_out - 300, n_out)):
+        want = sum(dy[t, r].float()[:, None] * x[t].float()[None, :] for t in range(tokens))
+        assert torch.equal(dw[r], want)

@@ -173,3 +173,19 @@ def test_lookup_and_gradient_are_adjoint():
     zs.zero_embed_grad(dw, dy.t, ids.to(DEV), scale=2.0, workspace=ws)
     left = (out.double() * dy.t.double().nan_to_num(0.0)).sum().item()
     assert left == (W.double() * dw.cpu().double()).sum().item()
+
+
+def test_gradient_rows_past_4_gib():
+    # a table gradient of 5.4 GB and dy of 4.4 GB: offsets past 2^32 on both sides
+    vocab, width, tokens = 330_000, 4096, 540_000
+    ids = torch.full((tokens,), vocab - 2, dtype=torch.int32, device=DEV)
+    ids[::1000] = vocab - 1
+    ids[1::1000] = 0
+    dy = torch.zeros(tokens, width, dtype=torch.bfloat16, device=DEV)
+    dy[-1], dy[-1000], dy[-999] = 1.0, 2.0, 4.0     # ids vocab - 2, vocab - 1 and 0
+    ws = torch.empty(zs.zero_embed_grad_workspace(tokens, vocab, width), dtype=torch.uint8,
+                     device=DEV)
+    dw = torch.full((vocab, width), 3.0, device=DEV)
+    zs.zero_embed_grad(dw, dy, ids, workspace=ws)
+    assert bool((dw[vocab - 2] == 1).all()) and bool((dw[vocab - 1] == 2).all())
+    assert bool((dw[0] == 4).all()) and not bool(dw[1:vocab - 2].any())

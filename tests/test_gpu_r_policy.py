@@ -74,7 +74,8 @@ def check(got, z, a, old, ref, adv, w, kl, S, dt, what=""):
 # vocabularies around every block size's edge, one to many rows
 SHAPES = [(1, 1), (3, 2), (5, 7), (4, 8), (6, 9), (9, 511), (7, 1024), (3, 1025), (5, 2047),
           (4, 4096), (3, 8193), (2, 16385), (3, 32771), (2, 50257), (2, 65537), (2, 131072),
-          (2, 131073), (1, 200_003), (40, 300), (130, 65)]
+          (2, 131073), (1, 200_003), (40, 300), (130, 65), (3, 49_153), (2, 98_305), (1, 262_144),
+          (2, 262_161), (1, 300_007)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
@@ -91,7 +92,8 @@ def test_loss_and_gradient(rows, vocab, dt):
 
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("rows,vocab,gap,lead", [(5, 100, 0, 1), (4, 3001, 3, 2), (3, 50257, 0, 5),
-                                                 (2, 200_003, 1, 3), (2, 24_576, 0, 7)])
+                                                 (2, 200_003, 1, 3), (2, 24_576, 0, 7),
+                                                 (2, 270_001, 5, 1)])
 def test_in_place_equals_apart(rows, vocab, gap, lead, dt):
     x = inputs(rows, vocab, dt, 5)
     apart = run(*x, 0.05, 64.0, gap=gap, lead=lead)
@@ -102,7 +104,7 @@ def test_in_place_equals_apart(rows, vocab, gap, lead, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("vocab", [60, 5000, 40_000, 250_000])
+@pytest.mark.parametrize("vocab", [60, 5000, 40_000, 250_000, 280_000])
 def test_on_policy_and_without_kl(vocab, dt):
     z, a, old, ref, adv, w = inputs(4, vocab, dt, 6)
     x = (z, a, None, None, adv, w)
@@ -113,7 +115,7 @@ def test_on_policy_and_without_kl(vocab, dt):
     check(run(*x, 0.3, 2.0), *x, 0.3, 2.0, dt)
 
 
-@pytest.mark.parametrize("vocab", [40, 3000, 30_000, 250_000])
+@pytest.mark.parametrize("vocab", [40, 3000, 30_000, 250_000, 280_000])
 def test_skipped_rows_are_not_read(vocab):
     z, a, old, ref, adv, w = inputs(6, vocab, "bf16", 7, masked=False)
     w[1] = w[4] = 0.0
@@ -131,8 +133,8 @@ def test_skipped_rows_are_not_read(vocab):
     assert float(none[0]) == 0.0 and bool((none[3] == 0).all())
 
 
-@pytest.mark.parametrize("vocab", [40, 3000, 30_000, 250_000])
-@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("vocab", [40, 3000, 30_000, 250_000, 280_000])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 def test_excluded_tokens_and_bad_rows(vocab, dt):
     z, a, old, ref, adv, w = inputs(8, vocab, dt, 8, masked=False)
     ninf, inf, nan = -float("inf"), float("inf"), float("nan")
@@ -237,3 +239,66 @@ def test_logits_past_4_gib():
                         loss_scale=2.0, dlogits=dz)
     check((loss, token[-3:], logp[-3:], dz[-3:]), h, a, old, ref, adv, w, 0.1, 2.0, "bf16")
     assert not bool(dz[:-3].any())
+
+
+@pytest.mark.parametrize("vocab", [50, 20_000, 270_000])
+def test_unusual_arguments(vocab):
+    # no upper cut, a full lower one, a negative KL weight, negative weights, int32 targets
+    z, a, old, ref, adv, w = inputs(6, vocab, "f32", 15, masked=False)
+    w[2] = -w[2]
+    f = lambda lo, hi, kl, t: (lambda o: (zs.zero_policy_loss(
+        o[0], o[1], o[2], z.to(DEV), t.to(DEV), adv.to(DEV), w.to(DEV), old_logp=old.to(DEV),
+        ref_logp=ref.to(DEV), clip_low=lo, clip_high=hi, kl_coef=kl, loss_scale=2.0,
+        dlogits=o[3]), o)[1])([torch.empty(1, device=DEV), torch.empty(6, device=DEV),
+                               torch.empty(6, device=DEV), torch.empty(6, vocab, device=DEV)])
+    n = lambda t: t.double().numpy()
+    for lo, hi, kl in ((1.0, float("inf"), 0.1), (0.0, 0.0, -0.2)):
+        got = f(lo, hi, kl, a)
+        ex = plain.policy(n(z), a.numpy(), n(old), n(ref), n(adv), n(w), lo, hi, kl, 2.0)
+        far = ~ex["near"]
+        err = np.abs(plain.f64(got[3]) - ex["dlogits"])
+        # the bounds count kl by its magnitude
+        bound = plain.policy(n(z), a.numpy(), n(old), n(ref), n(adv), n(w), lo, hi, abs(kl), 2.0)
+        tol = plain.rounded(np.maximum(np.abs(ex["dlogits"]), np.abs(bound["dlogits"])),
+                            bound["b_dlogits"], "f32") + np.abs(bound["dlogits"]) * 8 * plain.U
+        assert np.all(err[far] <= tol[far])
+        for p, q in zip(got, f(lo, hi, kl, a.int())):
+            assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("vocab", [40, 3000, 30_000, 250_000, 280_000])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_large_logits(vocab, dt):
+    # rows far from zero up to the end of the range: the terms go by z - m
+    td = plain.TORCH[dt]
+    for v in (2.0 ** 19, 2.0 ** 21, 1e12, 1e38, 3e38):
+        z = torch.zeros(3, vocab, dtype=td)
+        z[0, 3], z[1, 5] = v, -v
+        z[2] = v
+        z[2, 7] = -v
+        a, one = torch.tensor([3, 3, 4]), torch.ones(3)
+        for in_place in (False, True):
+            loss, token, logp, dl = run(z, a, None, None, one, one, 0.0, 1.0, in_place=in_place)
+            assert float(logp[0]) == 0.0 and bool((dl[0] == 0).all())
+            for r in (1, 2):        # one token of the row excluded, the others alike
+                p = 1.0 / (vocab - 1)
+                assert abs(float(logp[r]) + np.log(vocab - 1)) <= 40 * plain.U * np.log(vocab)
+                assert float(dl[r, 5 if r == 1 else 7]) == 0.0
+                tol = plain.rounded(np.float64(p), p * (208 + vocab / 1024) * plain.U, dt)
+                assert abs(float(dl[r, 0]) - p) <= tol, (v, r)
+
+
+def test_rows_past_the_sum_kernels_stride():
+    # more rows than the loss's sum takes at once: whole numbers, an exact total
+    rows = 30_011
+    z = torch.zeros(rows, 2, device=DEV)
+    t = torch.zeros(rows, dtype=torch.int64, device=DEV)
+    w = torch.ones(rows, device=DEV)
+    w[::7] = 0
+    adv = (torch.arange(rows, device=DEV) % 5).float()
+    loss, token, logp = torch.empty(1, device=DEV), torch.empty(rows, device=DEV), \
+        torch.empty(rows, device=DEV)
+    zs.zero_policy_loss(loss, token, logp, z, t, adv, w, clip_low=0.2, clip_high=0.2, kl_coef=0.0,
+                        loss_scale=1.0)
+    assert torch.equal(token, torch.where(w != 0, -adv, torch.zeros_like(adv)))
+    assert float(loss) == -float((adv * w).double().sum())

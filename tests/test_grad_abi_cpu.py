@@ -3,6 +3,9 @@ code before anything touches a device, and empty calls are no-ops.
 
 Pointers are made up and never dereferenced.
 """
+import os
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -10,6 +13,7 @@ import torch
 import grad_plain as plain
 import zero_sharded_mixed_shard_amd as zs
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 EINVAL, EDTYPE = -1, -2
 A = 0x10_0000_0000          # far-apart, 256-B aligned made-up addresses
 STEP = 1 << 32
@@ -199,3 +203,32 @@ def test_plain_checkpoint_is_exact_in_its_format_and_within_its_bound(dt):
     bound = np.maximum(np.abs(xd) * 2.0 ** -4, np.ldexp(1.0, k - 10))
     assert np.all(np.abs(v - xd)[fin] <= bound[fin])
     assert e.min() >= 3 and e.max() <= 247
+
+
+# ---- the header and the host side ---------------------------------------------------------
+
+def test_header_is_plain_c(tmp_path):
+    src = tmp_path / "t.c"
+    src.write_text('#include "zero_shard_grad.h"\n'
+                   "int main(void) { return ZERO_ACT_BLOCK - 32 + ZERO_ACT_NONE + ZERO_I32; }\n")
+    r = subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-pedantic", "-I",
+                        os.path.join(ROOT, "include"), str(src), "-o", str(tmp_path / "t")],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_fast_division_under_sanitizers(tmp_path):
+    inc = "/opt/rocm/include"
+    driver = os.path.join(ROOT, "tests", "sanitize", "fast_div_driver.cpp")
+    if not os.path.exists(os.path.join(inc, "hip", "hip_runtime_api.h")) or \
+            not os.path.exists(driver):
+        pytest.skip("HIP headers or the driver not found")
+    exe = tmp_path / "fast_div_driver"
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined",
+                        "-fno-sanitize-recover=all", "-static-libasan", "-static-libubsan",
+                        "-D__HIP_PLATFORM_AMD__", "-I", inc, "-I", os.path.join(ROOT, "include"),
+                        "-I", os.path.join(ROOT, "zero_sharded_mixed_shard_amd", "csrc"), driver,
+                        "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", (r.stdout, r.stderr[-2000:])

@@ -620,7 +620,8 @@ extern "C" const char *zero_strerror(int code) {
         case ZERO_EINVAL:
             return "invalid argument";
         case ZERO_EDTYPE:
-            return "unsupported dtype (ZERO_F16 or ZERO_BF16; the exchanges also take ZERO_F32)";
+            return "unsupported dtype (ZERO_F16 or ZERO_BF16; the exchanges, activations, lookups and "
+                   "the policy loss also take ZERO_F32; ids are ZERO_I32 or ZERO_I64)";
         case ZERO_EHIP:
             return g_err[0] ? g_err : "HIP runtime error";
         case ZERO_ERANGE:

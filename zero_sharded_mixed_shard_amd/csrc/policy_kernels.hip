@@ -13,7 +13,9 @@
 // The arithmetic matters next to the memory: an element takes a packed maximum,
 // two fused multiply-adds and two 2^x.  e^(z - m) is taken as 2^(z log2 e - c) with
 // c = m log2 e rounded: that rounding scales every term and the sum alike, and the
-// log-probability is formed with the same c, so it cancels.
+// log-probability is formed with the same c, so it cancels.  A row whose maximum is
+// not within 2^20 (where the scaling stays below 2^0.1), infinities and NaN among them,
+// is read again and takes (z - m) log2 e.
 //
 // Rows start anywhere: vectors are taken at the 16-B boundaries of the row, and the
 // fewer than 2 * 8 elements before the first and after the last whole vector one a
@@ -33,10 +35,20 @@ template <int F> constexpr int kPer = F == 2 ? 4 : 8;   // logits of a 16-B vect
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// e^(z - m), c = m log2 e.
-__device__ __forceinline__ float exp_from(float z, float c) {
-    return __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -c));
-}
+// e^(z - m): with c = m log2 e folded in, and by the difference.
+struct Folded {
+    float c;
+    __device__ __forceinline__ float operator()(float z) const {
+        return __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -c));
+    }
+};
+struct Plain {
+    float m;
+    __device__ __forceinline__ float operator()(float z) const {
+        return __builtin_amdgcn_exp2f((z - m) * kLog2e);
+    }
+};
+constexpr float kFoldLimit = 0x1p20f;
 
 // The largest logit, from the bit patterns: non-negative floats order like signed
 // integers, and among negative ones the largest has the smallest unsigned pattern.
@@ -169,7 +181,6 @@ __device__ __forceinline__ float block_reduce(float x, float *red) {
 
 // What a row's gradient needs, the same in every lane.
 struct RowGrad {
-    float c;        // largest logit times log2 e
     float scale;    // -S w g / sum
     float hit;      // S w g, added at the target
 };
@@ -185,7 +196,7 @@ __device__ __forceinline__ float exp_minus_1(float d) {
     for (int n = 12; n >= 2; --n) s = __builtin_fmaf(d * (1.0f / n), s, 1.0f);
     return d * s;
 }
-__device__ __forceinline__ float exp_of(float x) {
+__device__ __forceinline__ float exp_near(float x) {
     return __builtin_fabsf(x) <= 1.0f ? 1.0f + exp_minus_1(x) : exp_fast(x);
 }
 
@@ -212,21 +223,20 @@ __device__ __forceinline__ double log_of(float x) {
     return static_cast<double>(k) * 0.693147180559945309417 + static_cast<double>(ln_f);
 }
 
-// The row's loss from its maximum m, c = m log2 e as rounded, and the sum of
-// 2^(z log2 e - c); lane 0 writes token_loss and logp.  Losses of both signs cancel in
-// the total, so the log-probability and its distances to the old and the reference one
-// are taken in FP64: c's rounding, m log2 e - c, is known exactly from one fused
-// operation, and what is left is the sum's own error.
-__device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, float m, float c,
+// The row's loss from its maximum m and the sum of its terms, which hold a factor
+// 2^rest; lane 0 writes token_loss and logp.  Losses of both signs cancel in the total,
+// so the log-probability and its distances to the old and the reference one are taken in
+// FP64: rest = m log2 e - c is known exactly from one fused operation, and what is left
+// is the sum's own error.
+__device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, float m, float rest,
                                               float sum, float z_target, float w, uint32_t lane) {
-    const double rest = static_cast<double>(__builtin_fmaf(m, kLog2e, -c)) * 0.693147180559945309417;
     const double lp = (static_cast<double>(z_target) - static_cast<double>(m)) -
-                      (log_of(sum) - rest);
+                      (log_of(sum) - static_cast<double>(rest) * 0.693147180559945309417);
     const float logp = static_cast<float>(lp);
     const float A = a.advantage[t];
     float r = 1.0f;
     if (a.old_logp != nullptr)
-        r = exp_of(static_cast<float>(lp - static_cast<double>(a.old_logp[t])));
+        r = exp_near(static_cast<float>(lp - static_cast<double>(a.old_logp[t])));
     const float lo = 1.0f - a.clip_low, hi = 1.0f + a.clip_high;
     float rc = r < lo ? lo : r;
     rc = rc > hi ? hi : rc;
@@ -246,7 +256,7 @@ __device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, f
     }
     const float S = a.loss_scale_dev != nullptr ? *a.loss_scale_dev : a.loss_scale;
     const float h = S * (w * g);
-    return RowGrad{c, -h / sum, h};
+    return RowGrad{-h / sum, h};
 }
 
 // The target's logit, NaN for a target outside the vocabulary (at: its index,
@@ -285,15 +295,15 @@ __device__ __forceinline__ void skip_row(const PolicyArgs &a, uint64_t t) {
 }
 
 // Gradients of vector first + lane from its logits.
-template <int F>
+template <int F, typename Exp>
 __device__ __forceinline__ void grad_vec(elem_t<F> *d, uint32_t head, uint32_t first,
-                                         uint32_t lane, const u32x4 &w, const RowGrad &g,
-                                         uint32_t target) {
+                                         uint32_t lane, const u32x4 &w, const Exp &exp_of,
+                                         const RowGrad &g, uint32_t target) {
     constexpr uint32_t K = kPer<F>;
     float z[K];
     widen_vec<F>(w, z);
 #pragma unroll
-    for (uint32_t i = 0; i < K; ++i) z[i] = exp_from(z[i], g.c) * g.scale;
+    for (uint32_t i = 0; i < K; ++i) z[i] = exp_of(z[i]) * g.scale;
     // the target's place among the vectors (it wraps to none for an edge element)
     const uint32_t at = target - head;
     if (at / K - first == lane) {
@@ -303,12 +313,33 @@ __device__ __forceinline__ void grad_vec(elem_t<F> *d, uint32_t head, uint32_t f
     store_vec_at<F>(d, head, first, lane, z);
 }
 
-template <int F>
-__device__ __forceinline__ void grad_edge(elem_t<F> *d, uint32_t edge, float z, const RowGrad &g,
-                                          uint32_t target) {
+template <int F, typename Exp>
+__device__ __forceinline__ void grad_edge(elem_t<F> *d, uint32_t edge, float z, const Exp &exp_of,
+                                          const RowGrad &g, uint32_t target) {
     if (edge == ~0u) return;
-    const float p = exp_from(z, g.c) * g.scale;
+    const float p = exp_of(z) * g.scale;
     d[edge] = from_f32<F>(edge == target ? p + g.hit : p);
+}
+
+// Row t by reading it again, once its maximum m is known: the sum, then the gradients.
+template <int F, int T>
+__device__ __forceinline__ void reread_row(const PolicyArgs &a, uint64_t t, const elem_t<F> *row,
+                                           const Row<F> &r, float m, float zt, uint32_t target,
+                                           float ze, float weight, uint32_t lane, float *red) {
+    const Plain exp_of{m};
+    float s = r.edge != ~0u ? exp_of(ze) : 0.0f;
+    for (uint32_t j = 0; j + lane < r.n_vec; j += T) {
+        float z[kPer<F>];
+        widen_vec<F>(vec_at<F>(row, r.head, j, lane), z);
+#pragma unroll
+        for (int k = 0; k < kPer<F>; ++k) s = s + exp_of(z[k]);
+    }
+    s = block_reduce<T, false>(s, red);
+    const RowGrad g = finish_row(a, t, m, 0.0f, s, zt, weight, lane);
+    auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
+    for (uint32_t j = 0; j + lane < r.n_vec; j += T)
+        grad_vec<F>(d, r.head, j, lane, vec_at<F>(row, r.head, j, lane), exp_of, g, target);
+    grad_edge<F>(d, r.edge, ze, exp_of, g, target);
 }
 
 // A block of 64 lanes a row would be bound by the rate at which blocks start: rows
@@ -384,13 +415,18 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
         const float ze = r.edge != ~0u ? to_f32<F>(row[r.edge]) : -kInf;
 #pragma unroll
         for (int i = 0; i < N; ++i) take(x[i]);
-        const float m = block_reduce<T, true>(max_nan(most.value(), ze), red), c = m * kLog2e;
-        float s = exp_from(ze, c);
+        const float m = block_reduce<T, true>(max_nan(most.value(), ze), red);
+        if (!(__builtin_fabsf(m) <= kFoldLimit)) {   // the same in every lane of the row
+            reread_row<F, T>(a, t, row, r, m, zt, target, ze, weight, lane, red);
+            continue;
+        }
+        const Folded exp_of{m * kLog2e};
+        float s = exp_of(ze);
         auto add = [&](const u32x4 &w) {
             float z[kPer<F>];
             widen_vec<F>(w, z);
 #pragma unroll
-            for (int k = 0; k < kPer<F>; ++k) s = s + exp_from(z[k], c);
+            for (int k = 0; k < kPer<F>; ++k) s = s + exp_of(z[k]);
         };
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -404,20 +440,21 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
             add(held[i][lane]);
         }
         s = block_reduce<T, false>(s, red);
-        const RowGrad g = finish_row(a, t, m, c, s, zt, weight, lane);
+        const RowGrad g = finish_row(a, t, m, __builtin_fmaf(m, kLog2e, -exp_of.c), s, zt, weight,
+                                     lane);
         auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
         asm volatile("" : "+s"(n_vec));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             keep_raw(x[i]);
-            if (on(i)) grad_vec<F>(d, r.head, i * T, lane, x[i], g, target);
+            if (on(i)) grad_vec<F>(d, r.head, i * T, lane, x[i], exp_of, g, target);
         }
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             __builtin_amdgcn_sched_barrier(0);
-            if (on(N + i)) grad_vec<F>(d, r.head, (N + i) * T, lane, held[i][lane], g, target);
+            if (on(N + i)) grad_vec<F>(d, r.head, (N + i) * T, lane, held[i][lane], exp_of, g, target);
         }
-        grad_edge<F>(d, r.edge, ze, g, target);
+        grad_edge<F>(d, r.edge, ze, exp_of, g, target);
     }
 }
 
@@ -440,9 +477,10 @@ __global__ __launch_bounds__(kBlock<T>) void policy_long_kernel(PolicyArgs a) {
         uint32_t target;
         const float zt = target_logit<F>(a, row, t, &target);
         const float ze = r.edge != ~0u ? to_f32<F>(row[r.edge]) : -kInf;
-        // the edge element's term is 1 in units of its own maximum (NaN if it is not finite)
-        float m = ze, c = m == -kInf ? 0.0f : m * kLog2e;   // c = m log2 e, 0 while m is -inf
-        float s = exp_from(ze, c);
+        // the running maximum and the sum in its units; nothing but -inf so far adds nothing.
+        // The edge element's term is 1 in its own units (NaN if it is infinite or NaN)
+        float m = ze;
+        float s = m == -kInf ? 0.0f : Plain{m}(ze);
         for (uint32_t j = 0; j + lane < r.n_vec; j += T) {
             const u32x4 w = vec_at<F>(row, r.head, j, lane);
             MaxBits<F> most;
@@ -450,27 +488,26 @@ __global__ __launch_bounds__(kBlock<T>) void policy_long_kernel(PolicyArgs a) {
             for (int k = 0; k < 4; ++k) most.take(w[k]);
             const float vm = max_nan(most.value(), m);
             if (vm != m) {           // the sum so far in units of the new maximum
-                s = m == -kInf ? s : s * exp_from(m, vm * kLog2e);
+                s = m == -kInf ? s : s * Plain{vm}(m);
                 m = vm;
-                c = m * kLog2e;
             }
+            const Plain exp_of{m == -kInf ? 0.0f : m};
             float z[K];
             widen_vec<F>(w, z);
 #pragma unroll
-            for (int k = 0; k < K; ++k) s = s + exp_from(z[k], c);
+            for (int k = 0; k < K; ++k) s = s + exp_of(z[k]);
         }
-        const float rm = block_reduce<T, true>(m, red), rc = rm * kLog2e;
-        // a lane's terms were scaled by its own rounded c
-        s = block_reduce<T, false>(
-            m == -kInf ? s : s * __builtin_amdgcn_exp2f(c - rc), red);
+        const float rm = block_reduce<T, true>(m, red);
+        const Plain exp_of{rm};
+        s = block_reduce<T, false>(m == -kInf ? s : s * exp_of(m), red);
         if (rm == -kInf) s = __builtin_nanf("");   // nothing left to choose from
-        const RowGrad g = finish_row(a, t, rm, rc, s, zt, weight, lane);
+        const RowGrad g = finish_row(a, t, rm, 0.0f, s, zt, weight, lane);
         if (a.dlogits == nullptr) continue;
         auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
         for (uint32_t j = 0; j + lane < r.n_vec; j += T)
-            grad_vec<F>(d, r.head, j, lane, vec_at<F>(row, r.head, j, lane), g,
+            grad_vec<F>(d, r.head, j, lane, vec_at<F>(row, r.head, j, lane), exp_of, g,
                         target);
-        grad_edge<F>(d, r.edge, ze, g, target);
+        grad_edge<F>(d, r.edge, ze, exp_of, g, target);
     }
 }
 
