@@ -194,7 +194,7 @@ int zero_embed_grad_workspace(uint64_t tokens, uint64_t vocab, uint64_t width, u
  *     d     = ref_logp - logp              (0 where ref_logp is NULL)
  *     L     = max(-r A, -clamp(r, 1 - clip_low, 1 + clip_high) A)
  *             + kl_coef * (e^d - d - 1)
- *     loss  = sum over t of w L            (FP64, in row order, rounded once)
+ *     loss  = sum over t of w L            (FP64, in a fixed order, rounded once)
  *     dlogits[v] = S w g ([v == a] - e^(z[v]) / sum)
  *     g     = kl_coef * (1 - e^d) - (0 where the clamp cuts r off, r A elsewhere)
  * where the clamp cuts off for A > 0 and r > 1 + clip_high, and for A < 0 and

@@ -112,8 +112,31 @@ def test_gradient_of_whole_numbers_is_exact(tokens, vocab, width, kind, dt):
     assert acc.intact() and torch.equal(d_ids.cpu(), ids)
 
 
+# few tokens in a large table: ids that crowd into one group of rows, runs on both sides of
+# 16 tokens, tables that end inside a group of 64 rows
+FEW = [(1024, 16_384, 48, "mixed"), (1024, 16_383, 48, "mixed"), (1025, 16_384, 48, "mixed"),
+       (1024, 262_144, 8, "mixed"), (1024, 262_145, 8, "mixed"), (1, 16_385, 1, "same"),
+       (1024, 20_000, 1030, "same"), (1023, 16_447, 520, "crowd"), (1000, 20_001, 512, "runs"),
+       (700, 17_000, 2051, "runs"), (512, 50_257, 768, "distinct"), (300, 16_400, 9, "outside"),
+       (65, 16_385, 777, "last")]
+
+
+@pytest.mark.parametrize("tokens,vocab,width,kind", FEW)
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
-@pytest.mark.parametrize("tokens,vocab,width", [(700, 50, 130), (30_000, 2000, 64)])
+def test_gradient_of_few_tokens_is_exact(tokens, vocab, width, kind, dt, monkeypatch):
+    special = {"crowd": lambda t: 64 * 7 + t % 64,            # 16 tokens a row, interleaved
+               "runs": lambda t: 63 + 5 * (t * (t + 1) % 33 % 11),   # rows of uneven counts
+               "last": lambda t: vocab - 1 - t % 3}
+    if kind in special:
+        make = special[kind]
+        monkeypatch.setitem(globals(), "ids_of", lambda n, v, s, k, dtype=torch.int64:
+                            torch.tensor([make(t) for t in range(n)]).to(dtype))
+    test_gradient_of_whole_numbers_is_exact(tokens, vocab, width, kind, dt)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("tokens,vocab,width",
+                         [(700, 50, 130), (30_000, 2000, 64), (1000, 20_000, 130)])
 def test_random_gradients_within_the_sum_bound_and_repeatable(tokens, vocab, width, dt):
     g = torch.Generator().manual_seed(3)
     h = torch.randn(tokens, width, generator=g).to(plain.TORCH[dt])

@@ -19,9 +19,9 @@
 //
 // Rows start anywhere: vectors are taken at the 16-B boundaries of the row, and the
 // fewer than 2 * 8 elements before the first and after the last whole vector one a
-// lane (lanes without a vector or an element hold -inf, which adds nothing).  dlogits may be logits: all of a row is on
-// chip before any of it is written, and the two-pass form writes an element after
-// its last read.
+// lane (lanes without a vector or an element hold -inf, which adds nothing).  dlogits
+// may be logits: all of a row is on chip before any of it is written, and the forms that
+// read a row twice write an element after its last read.
 #include "grad_device.h"
 
 #pragma clang fp contract(off)
@@ -179,6 +179,32 @@ __device__ __forceinline__ float block_reduce(float x, float *red) {
     return r;
 }
 
+// A value that no kernel of this call writes, at an address that is the same in every
+// lane: a scalar load, whose result waits in scalar registers until it is needed.
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T *p) {
+    return *(const __attribute__((address_space(4))) T *)(p);
+}
+
+// A row's own inputs, requested before its logits so that nothing waits for them later:
+// 16384 x 50257 BF16 rows 647 -> 604 us, 400000 x 1024 523 -> 417 us.
+struct RowIn {
+    float advantage, old_logp, ref_logp, loss_scale;
+    int64_t target;
+    __device__ __forceinline__ RowIn(const PolicyArgs &a, uint64_t t) {
+        advantage = uniform_load(a.advantage + t);
+        old_logp = a.old_logp != nullptr ? uniform_load(a.old_logp + t) : 0.0f;
+        ref_logp = a.ref_logp != nullptr ? uniform_load(a.ref_logp + t) : 0.0f;
+        loss_scale = a.loss_scale_dev != nullptr ? uniform_load(a.loss_scale_dev) : a.loss_scale;
+        target = a.targets64 ? uniform_load(static_cast<const int64_t *>(a.targets) + t)
+                             : uniform_load(static_cast<const int32_t *>(a.targets) + t);
+    }
+    // In scalar registers up to here: nothing made from them is held beside the row.
+    __device__ __forceinline__ void arrive() {
+        asm volatile("" : "+s"(advantage), "+s"(old_logp), "+s"(ref_logp), "+s"(loss_scale));
+    }
+};
+
 // What a row's gradient needs, the same in every lane.
 struct RowGrad {
     float scale;    // -S w g / sum
@@ -228,15 +254,17 @@ __device__ __forceinline__ double log_of(float x) {
 // so the log-probability and its distances to the old and the reference one are taken in
 // FP64: rest = m log2 e - c is known exactly from one fused operation, and what is left
 // is the sum's own error.
-__device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, float m, float rest,
-                                              float sum, float z_target, float w, uint32_t lane) {
+__device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, RowIn in, uint64_t t,
+                                              float m, float rest, float sum, float z_target,
+                                              float w, uint32_t lane) {
+    in.arrive();
     const double lp = (static_cast<double>(z_target) - static_cast<double>(m)) -
                       (log_of(sum) - static_cast<double>(rest) * 0.693147180559945309417);
     const float logp = static_cast<float>(lp);
-    const float A = a.advantage[t];
+    const float A = in.advantage;
     float r = 1.0f;
     if (a.old_logp != nullptr)
-        r = exp_near(static_cast<float>(lp - static_cast<double>(a.old_logp[t])));
+        r = exp_near(static_cast<float>(lp - static_cast<double>(in.old_logp)));
     const float lo = 1.0f - a.clip_low, hi = 1.0f + a.clip_high;
     float rc = r < lo ? lo : r;
     rc = rc > hi ? hi : rc;
@@ -245,7 +273,7 @@ __device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, f
     const bool cut = (A > 0.0f && r > hi) || (A < 0.0f && r < lo);
     float g = cut ? 0.0f : p0;
     if (a.ref_logp != nullptr && a.kl_coef != 0.0f) {
-        const float d = static_cast<float>(static_cast<double>(a.ref_logp[t]) - lp);
+        const float d = static_cast<float>(static_cast<double>(in.ref_logp) - lp);
         const float em = exp_minus_1(d);
         L = L + a.kl_coef * (em - d);
         g = g - a.kl_coef * em;
@@ -254,8 +282,7 @@ __device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, f
         a.token_loss[t] = L;
         a.logp[t] = logp;
     }
-    const float S = a.loss_scale_dev != nullptr ? *a.loss_scale_dev : a.loss_scale;
-    const float h = S * (w * g);
+    const float h = in.loss_scale * (w * g);
     return RowGrad{-h / sum, h};
 }
 
@@ -263,9 +290,7 @@ __device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, uint64_t t, f
 // ~0 then).
 template <int F>
 __device__ __forceinline__ float target_logit(const PolicyArgs &a, const elem_t<F> *row,
-                                              uint64_t t, uint32_t *at) {
-    const int64_t v = a.targets64 ? static_cast<const int64_t *>(a.targets)[t]
-                                  : static_cast<const int32_t *>(a.targets)[t];
+                                              int64_t v, uint32_t *at) {
     const bool in = v >= 0 && static_cast<uint64_t>(v) < a.vocab;
     *at = in ? static_cast<uint32_t>(v) : 0xffffffffu;
     return in ? to_f32<F>(row[v]) : __builtin_nanf("");
@@ -322,10 +347,17 @@ __device__ __forceinline__ void grad_edge(elem_t<F> *d, uint32_t edge, float z, 
 }
 
 // Row t by reading it again, once its maximum m is known: the sum, then the gradients.
+// Everything else is made anew from t, so that nothing is held for it beside a row on chip.
 template <int F, int T>
-__device__ __forceinline__ void reread_row(const PolicyArgs &a, uint64_t t, const elem_t<F> *row,
-                                           const Row<F> &r, float m, float zt, uint32_t target,
-                                           float ze, float weight, uint32_t lane, float *red) {
+__device__ __forceinline__ void reread_row(const PolicyArgs &a, uint64_t t, float m, float *red) {
+    uint32_t lane = lane_of<T>();
+    asm volatile("" : "+v"(lane));
+    const RowIn in(a, t);
+    const auto *row = static_cast<const elem_t<F> *>(a.logits) + t * a.ld;
+    const Row<F> r(row, static_cast<uint32_t>(a.vocab), lane);
+    uint32_t target;
+    const float zt = target_logit<F>(a, row, in.target, &target);
+    const float ze = r.edge != ~0u ? to_f32<F>(row[r.edge]) : -kInf;
     const Plain exp_of{m};
     float s = r.edge != ~0u ? exp_of(ze) : 0.0f;
     for (uint32_t j = 0; j + lane < r.n_vec; j += T) {
@@ -335,7 +367,7 @@ __device__ __forceinline__ void reread_row(const PolicyArgs &a, uint64_t t, cons
         for (int k = 0; k < kPer<F>; ++k) s = s + exp_of(z[k]);
     }
     s = block_reduce<T, false>(s, red);
-    const RowGrad g = finish_row(a, t, m, 0.0f, s, zt, weight, lane);
+    const RowGrad g = finish_row(a, in, t, m, 0.0f, s, zt, uniform_load(a.weight + t), lane);
     auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
     for (uint32_t j = 0; j + lane < r.n_vec; j += T)
         grad_vec<F>(d, r.head, j, lane, vec_at<F>(row, r.head, j, lane), exp_of, g, target);
@@ -363,7 +395,8 @@ __device__ __forceinline__ uint64_t row_stride() {
 // chip: N vectors a lane in registers and L in LDS.
 // Four waves a SIMD leave 128 registers a lane.  The longest rows spill some 30 of them
 // around the row's scalar part; three waves a SIMD with more vectors a lane (384 lanes x
-// (31 + 12)) measured a third slower, as the arithmetic then hides less.
+// (31 + 12)) measured a third slower, as the arithmetic then hides less.  8192 x 131072
+// BF16: 815 us, 5.3 TB/s.
 template <int F, int T, int N, int L>
 __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) {
     constexpr int B = 3;                  // vectors on their way to LDS at once
@@ -374,11 +407,12 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
     for (uint64_t t = first_row<T>(); t < a.rows; t += row_stride<T>()) {
         uint32_t lane = lane_of<T>();  // of the group; opaque, so that nothing made from it
         asm volatile("" : "+v"(lane)); // is held in registers from row to row
-        const float weight = a.weight[t];
+        const float weight = uniform_load(a.weight + t);
         if (weight == 0.0f) {
             skip_row<F, T>(a, t);
             continue;
         }
+        const RowIn in(a, t);
         const auto *row = static_cast<const elem_t<F> *>(a.logits) + t * a.ld;
         const Row<F> r(row, V, lane);
         // lane holds vector i * T + lane; n_vec is hidden between the passes, so that their
@@ -411,13 +445,13 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = fetch(i);
         uint32_t target;
-        const float zt = target_logit<F>(a, row, t, &target);
+        const float zt = target_logit<F>(a, row, in.target, &target);
         const float ze = r.edge != ~0u ? to_f32<F>(row[r.edge]) : -kInf;
 #pragma unroll
         for (int i = 0; i < N; ++i) take(x[i]);
         const float m = block_reduce<T, true>(max_nan(most.value(), ze), red);
         if (!(__builtin_fabsf(m) <= kFoldLimit)) {   // the same in every lane of the row
-            reread_row<F, T>(a, t, row, r, m, zt, target, ze, weight, lane, red);
+            reread_row<F, T>(a, t, m, red);
             continue;
         }
         const Folded exp_of{m * kLog2e};
@@ -440,8 +474,9 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
             add(held[i][lane]);
         }
         s = block_reduce<T, false>(s, red);
-        const RowGrad g = finish_row(a, t, m, __builtin_fmaf(m, kLog2e, -exp_of.c), s, zt, weight,
-                                     lane);
+        // beside the longest rows even these scalars cost a spill: asked for again there
+        const RowGrad g = finish_row(a, N > 16 ? RowIn(a, t) : in, t, m,
+                                     __builtin_fmaf(m, kLog2e, -exp_of.c), s, zt, weight, lane);
         auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
         asm volatile("" : "+s"(n_vec));
 #pragma unroll
@@ -459,7 +494,8 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
 }
 
 // One row a block of T lanes in one pass for the loss (running maximum and sum a
-// lane) and, with dlogits, a second for the gradients.
+// lane) and, with dlogits, a second for the gradients: 3.3 to 3.5 TB/s of the logits read
+// once and the gradients written once, where the rows on chip reach 5.
 template <int F, int T>
 __global__ __launch_bounds__(kBlock<T>) void policy_long_kernel(PolicyArgs a) {
     constexpr int K = kPer<F>;
@@ -472,10 +508,11 @@ __global__ __launch_bounds__(kBlock<T>) void policy_long_kernel(PolicyArgs a) {
             skip_row<F, T>(a, t);
             continue;
         }
+        const RowIn in(a, t);
         const auto *row = static_cast<const elem_t<F> *>(a.logits) + t * a.ld;
         const Row<F> r(row, V, lane);
         uint32_t target;
-        const float zt = target_logit<F>(a, row, t, &target);
+        const float zt = target_logit<F>(a, row, in.target, &target);
         const float ze = r.edge != ~0u ? to_f32<F>(row[r.edge]) : -kInf;
         // the running maximum and the sum in its units; nothing but -inf so far adds nothing.
         // The edge element's term is 1 in its own units (NaN if it is infinite or NaN)
@@ -501,7 +538,7 @@ __global__ __launch_bounds__(kBlock<T>) void policy_long_kernel(PolicyArgs a) {
         const Plain exp_of{rm};
         s = block_reduce<T, false>(m == -kInf ? s : s * exp_of(m), red);
         if (rm == -kInf) s = __builtin_nanf("");   // nothing left to choose from
-        const RowGrad g = finish_row(a, t, rm, 0.0f, s, zt, weight, lane);
+        const RowGrad g = finish_row(a, in, t, rm, 0.0f, s, zt, weight, lane);
         if (a.dlogits == nullptr) continue;
         auto *d = static_cast<elem_t<F> *>(a.dlogits) + t * a.ldd;
         for (uint32_t j = 0; j + lane < r.n_vec; j += T)
