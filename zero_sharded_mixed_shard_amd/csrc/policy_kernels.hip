@@ -487,7 +487,8 @@ __global__ __launch_bounds__(kBlock<T>, 4) void policy_row_kernel(PolicyArgs a) 
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             __builtin_amdgcn_sched_barrier(0);
-            if (on(N + i)) grad_vec<F>(d, r.head, (N + i) * T, lane, held[i][lane], exp_of, g, target);
+            if (on(N + i))
+                grad_vec<F>(d, r.head, (N + i) * T, lane, held[i][lane], exp_of, g, target);
         }
         grad_edge<F>(d, r.edge, ze, exp_of, g, target);
     }

@@ -20,6 +20,9 @@
 //
 // Few tiles: the tokens are split over several blocks of a tile, which write FP32
 // partial products; a second kernel adds them in split order.
+//
+// What bounds it: the matrix cores, at the clock they leave (62% busy at 1.78 GHz).
+// 16384 x 8192 x 4096 BF16: 866 us, 1.27 PFLOP/s.
 #include "grad_device.h"
 
 #pragma clang fp contract(off)
@@ -34,7 +37,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
 
 template <int F>
 __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
@@ -161,295 +163,299 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void weight_grad_kernel(
     __shared__ __align__(16) uint16_t sb[2][kStep * BN];
 
     for (uint64_t work = blockIdx.x; work < g.work; work += gridDim.x) {
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-    uint32_t tile_o, tile_i;
-    if (!tile_of(g, work, &tile_o, &tile_i)) continue;
-    const uint32_t o0 = tile_o * BM, i0 = tile_i * BN;
-    const uint64_t t_first = static_cast<uint64_t>(blockIdx.y) * g.per_split;
-    const uint32_t t_begin = static_cast<uint32_t>(t_first < g.tokens ? t_first : g.tokens);
-    const uint32_t t_end = static_cast<uint32_t>(
-        t_first + g.per_split < g.tokens ? t_first + g.per_split : g.tokens);
-    const uint32_t steps = (t_end - t_begin + kStep - 1) / kStep;
+        const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+        uint32_t tile_o, tile_i;
+        if (!tile_of(g, work, &tile_o, &tile_i)) continue;
+        const uint32_t o0 = tile_o * BM, i0 = tile_i * BN;
+        const uint64_t t_first = static_cast<uint64_t>(blockIdx.y) * g.per_split;
+        const uint32_t t_begin = static_cast<uint32_t>(t_first < g.tokens ? t_first : g.tokens);
+        const uint32_t t_end = static_cast<uint32_t>(
+            t_first + g.per_split < g.tokens ? t_first + g.per_split : g.tokens);
+        const uint32_t steps = (t_end - t_begin + kStep - 1) / kStep;
 
-    // staging: this thread's eight columns and first row of each tile
-    const uint32_t ca = threadIdx.x % (BM / 8) * 8, ra = threadIdx.x / (BM / 8);
-    const uint32_t cb = threadIdx.x % (BN / 8) * 8, rb = threadIdx.x / (BN / 8);
-    const uint32_t na = TINY ? (o0 + ca < g.n_out ? g.n_out - o0 - ca : 0u) : 8u;
-    const uint32_t nb = TINY ? (i0 + cb < g.n_in ? g.n_in - i0 - cb : 0u) : 8u;
-    const uint32_t col_a = TINY || o0 + ca + 8 <= g.n_out ? o0 + ca : g.n_out - 8;
-    const uint32_t col_b = TINY || i0 + cb + 8 <= g.n_in ? i0 + cb : g.n_in - 8;
-    const uint32_t blk_b = (i0 + cb < g.n_in ? i0 + cb : g.n_in - 1) / ZERO_ACT_BLOCK;
-    // offsets of a lane from a row's start that is the same in every lane: 32 bits
-    // (the launcher checks that kStep rows stay below 4 GiB; TINY takes any)
-    using Off = typename Offset<TINY>::T;
-    u32x4 xa[PA];
-    u32x2 xb[PB];
-    uint32_t eb[PB];
-    auto get_a = [&](const uint16_t *row, Off off) {
-        const GLOBAL_AS uint16_t *s = at_offset(row, off * 2);
-        if constexpr (!TINY) return *(const GLOBAL_AS u32x4_any *)(s);
-        u32x4 r{0u, 0u, 0u, 0u};
+        // staging: this thread's eight columns and first row of each tile
+        const uint32_t ca = threadIdx.x % (BM / 8) * 8, ra = threadIdx.x / (BM / 8);
+        const uint32_t cb = threadIdx.x % (BN / 8) * 8, rb = threadIdx.x / (BN / 8);
+        const uint32_t na = TINY ? (o0 + ca < g.n_out ? g.n_out - o0 - ca : 0u) : 8u;
+        const uint32_t nb = TINY ? (i0 + cb < g.n_in ? g.n_in - i0 - cb : 0u) : 8u;
+        const uint32_t col_a = TINY || o0 + ca + 8 <= g.n_out ? o0 + ca : g.n_out - 8;
+        const uint32_t col_b = TINY || i0 + cb + 8 <= g.n_in ? i0 + cb : g.n_in - 8;
+        const uint32_t blk_b = (i0 + cb < g.n_in ? i0 + cb : g.n_in - 1) / ZERO_ACT_BLOCK;
+        // offsets of a lane from a row's start that is the same in every lane: 32 bits
+        // (the launcher checks that kStep rows stay below 4 GiB; TINY takes any)
+        using Off = typename Offset<TINY>::T;
+        u32x4 xa[PA];
+        u32x2 xb[PB];
+        uint32_t eb[PB];
+        auto get_a = [&](const uint16_t *row, Off off) {
+            const GLOBAL_AS uint16_t *s = at_offset(row, off * 2);
+            if constexpr (!TINY) return *(const GLOBAL_AS u32x4_any *)(s);
+            u32x4 r{0u, 0u, 0u, 0u};
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j)
-            if (j < na) r[j / 2] |= static_cast<uint32_t>(s[j]) << (16 * (j % 2));
-        return r;
-    };
-    auto get_b = [&](const uint8_t *row, Off off) {
-        const GLOBAL_AS uint8_t *s = at_offset(row, off);
-        if constexpr (!TINY) return *(const GLOBAL_AS u32x2_any *)(s);
-        u32x2 r{0u, 0u};
+            for (uint32_t j = 0; j < 8; ++j)
+                if (j < na) r[j / 2] |= static_cast<uint32_t>(s[j]) << (16 * (j % 2));
+            return r;
+        };
+        auto get_b = [&](const uint8_t *row, Off off) {
+            const GLOBAL_AS uint8_t *s = at_offset(row, off);
+            if constexpr (!TINY) return *(const GLOBAL_AS u32x2_any *)(s);
+            u32x2 r{0u, 0u};
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j)
-            if (j < nb) r[j / 4] |= static_cast<uint32_t>(s[j]) << (8 * (j % 4));
-        return r;
-    };
-    const Off off_a = static_cast<Off>(ra) * static_cast<Off>(g.lddy) + col_a;
-    const Off off_b = static_cast<Off>(rb) * g.n_in + col_b;
-    const Off off_e = static_cast<Off>(rb) * g.blocks_in + blk_b;
-    // step s into registers: a whole step, or (load_last) the last, perhaps short, one
-    auto load_a = [&](uint32_t s) {
-        const uint16_t *row = dy + static_cast<uint64_t>(t_begin + s * kStep) * g.lddy;
+            for (uint32_t j = 0; j < 8; ++j)
+                if (j < nb) r[j / 4] |= static_cast<uint32_t>(s[j]) << (8 * (j % 4));
+            return r;
+        };
+        const Off off_a = static_cast<Off>(ra) * static_cast<Off>(g.lddy) + col_a;
+        const Off off_b = static_cast<Off>(rb) * g.n_in + col_b;
+        const Off off_e = static_cast<Off>(rb) * g.blocks_in + blk_b;
+        // step s into registers: a whole step, or (load_last) the last, perhaps short, one
+        auto load_a = [&](uint32_t s) {
+            const uint16_t *row = dy + static_cast<uint64_t>(t_begin + s * kStep) * g.lddy;
 #pragma unroll
-        for (int p = 0; p < PA; ++p)
-            xa[p] = get_a(row + static_cast<uint64_t>(p * kRowsA) * g.lddy, off_a);
-    };
-    auto load_b = [&](uint32_t s) {
-        const uint64_t t0 = t_begin + s * kStep;
+            for (int p = 0; p < PA; ++p)
+                xa[p] = get_a(row + static_cast<uint64_t>(p * kRowsA) * g.lddy, off_a);
+        };
+        auto load_b = [&](uint32_t s) {
+            const uint64_t t0 = t_begin + s * kStep;
 #pragma unroll
-        for (int p = 0; p < PB; ++p) {
-            xb[p] = get_b(q + (t0 + p * kRowsB) * g.n_in, off_b);
-            eb[p] = *at_offset(e + (t0 + p * kRowsB) * g.blocks_in, off_e);
-        }
-    };
-    auto load_last = [&](uint32_t s) {
-        const uint32_t t0 = t_begin + s * kStep, last = t_end - 1 - t0;
+            for (int p = 0; p < PB; ++p) {
+                xb[p] = get_b(q + (t0 + p * kRowsB) * g.n_in, off_b);
+                eb[p] = *at_offset(e + (t0 + p * kRowsB) * g.blocks_in, off_e);
+            }
+        };
+        auto load_last = [&](uint32_t s) {
+            const uint32_t t0 = t_begin + s * kStep, last = t_end - 1 - t0;
 #pragma unroll
-        for (int p = 0; p < PA; ++p) {
-            const uint32_t t = ra + p * kRowsA, u = t < last ? t : last;
-            xa[p] = get_a(dy + static_cast<uint64_t>(t0) * g.lddy,
-                          static_cast<Off>(u) * static_cast<Off>(g.lddy) + col_a);
-            if (t > last) xa[p] = u32x4{0u, 0u, 0u, 0u};
-        }
+            for (int p = 0; p < PA; ++p) {
+                const uint32_t t = ra + p * kRowsA, u = t < last ? t : last;
+                xa[p] = get_a(dy + static_cast<uint64_t>(t0) * g.lddy,
+                              static_cast<Off>(u) * static_cast<Off>(g.lddy) + col_a);
+                if (t > last) xa[p] = u32x4{0u, 0u, 0u, 0u};
+            }
 #pragma unroll
-        for (int p = 0; p < PB; ++p) {
-            const uint32_t t = rb + p * kRowsB, u = t < last ? t : last;
-            xb[p] = get_b(q + static_cast<uint64_t>(t0) * g.n_in,
-                          static_cast<Off>(u) * g.n_in + col_b);
-            eb[p] = *at_offset(e + static_cast<uint64_t>(t0) * g.blocks_in,
-                               static_cast<Off>(u) * g.blocks_in + blk_b);
-            if (t > last) xb[p] = u32x2{0u, 0u};
-        }
-    };
-    auto load = [&](uint32_t s) {
-        if (s + 1 == steps) {
-            load_last(s);
-        } else {
-            load_a(s);
-            load_b(s);
-        }
-    };
-    // LDS place of eight columns c of row r in a tile of `width` columns
-    auto place = [](uint32_t r, uint32_t c, uint32_t width) {
-        const uint32_t turn = width >= 128 ? (r & 3u) << 1 : r & 2u;
-        return r * width + (((c >> 4) ^ turn) << 4) + (c & 15u);
-    };
-    auto stage_a = [&](uint32_t buf) {
+            for (int p = 0; p < PB; ++p) {
+                const uint32_t t = rb + p * kRowsB, u = t < last ? t : last;
+                xb[p] = get_b(q + static_cast<uint64_t>(t0) * g.n_in,
+                              static_cast<Off>(u) * g.n_in + col_b);
+                eb[p] = *at_offset(e + static_cast<uint64_t>(t0) * g.blocks_in,
+                                   static_cast<Off>(u) * g.blocks_in + blk_b);
+                if (t > last) xb[p] = u32x2{0u, 0u};
+            }
+        };
+        auto load = [&](uint32_t s) {
+            if (s + 1 == steps) {
+                load_last(s);
+            } else {
+                load_a(s);
+                load_b(s);
+            }
+        };
+        // LDS place of eight columns c of row r in a tile of `width` columns
+        auto place = [](uint32_t r, uint32_t c, uint32_t width) {
+            const uint32_t turn = width >= 128 ? (r & 3u) << 1 : r & 2u;
+            return r * width + (((c >> 4) ^ turn) << 4) + (c & 15u);
+        };
+        auto stage_a = [&](uint32_t buf) {
 #pragma unroll
-        for (int p = 0; p < PA; ++p)
-            *reinterpret_cast<u32x4 *>(&sa[buf][place(ra + p * kRowsA, ca, BM)]) = xa[p];
-    };
-    auto stage_b = [&](uint32_t buf) {
+            for (int p = 0; p < PA; ++p)
+                *reinterpret_cast<u32x4 *>(&sa[buf][place(ra + p * kRowsA, ca, BM)]) = xa[p];
+        };
+        auto stage_b = [&](uint32_t buf) {
 #pragma unroll
-        for (int p = 0; p < PB; ++p)
-            *reinterpret_cast<u32x4 *>(&sb[buf][place(rb + p * kRowsB, cb, BN)]) =
-                codes_to_16<F>(xb[p], eb[p]);
-    };
+            for (int p = 0; p < PB; ++p)
+                *reinterpret_cast<u32x4 *>(&sb[buf][place(rb + p * kRowsB, cb, BN)]) =
+                    codes_to_16<F>(xb[p], eb[p]);
+        };
 
-    // reading: lane (half, group of 16, j) reads row 8 half + j/4 (+4), columns
-    // 16 group + 4 (j mod 4) of a 32-column unit
-    const uint32_t half = lane >> 5, grp = (lane >> 4) & 1u, j = lane & 15u;
-    const uint32_t am = wave % WM * (BM / WM), bn = wave / WM * (BN / WN);
-    uint32_t pa[TM], pb[TN];
+        // reading: lane (half, group of 16, j) reads row 8 half + j/4 (+4), columns
+        // 16 group + 4 (j mod 4) of a 32-column unit
+        const uint32_t half = lane >> 5, grp = (lane >> 4) & 1u, j = lane & 15u;
+        const uint32_t am = wave % WM * (BM / WM), bn = wave / WM * (BN / WN);
+        uint32_t pa[TM], pb[TN];
 #pragma unroll
-    for (int m = 0; m < TM; ++m)
-        pa[m] = place(half * 8 + (j >> 2), am + m * 32 + grp * 16 + (j & 3u) * 4, BM);
-#pragma unroll
-    for (int n = 0; n < TN; ++n)
-        pb[n] = place(half * 8 + (j >> 2), bn + n * 32 + grp * 16 + (j & 3u) * 4, BN);
-    s16x8 a[2][TM], b[2][TN];
-    auto read = [&](int f, uint32_t buf, int kk) {
-#pragma unroll
-        for (int m = 0; m < TM; ++m) {
-            const s16x4 lo = read_tr(&sa[buf][pa[m] + kk * 16 * BM]);
-            const s16x4 hi = read_tr(&sa[buf][pa[m] + (kk * 16 + 4) * BM]);
-            a[f][m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-#pragma unroll
-        for (int n = 0; n < TN; ++n) {
-            const s16x4 lo = read_tr(&sb[buf][pb[n] + kk * 16 * BN]);
-            const s16x4 hi = read_tr(&sb[buf][pb[n] + (kk * 16 + 4) * BN]);
-            b[f][n] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-    };
-
-    f32x16 acc[TM][TN];
-#pragma unroll
-    for (int m = 0; m < TM; ++m)
+        for (int m = 0; m < TM; ++m)
+            pa[m] = place(half * 8 + (j >> 2), am + m * 32 + grp * 16 + (j & 3u) * 4, BM);
 #pragma unroll
         for (int n = 0; n < TN; ++n)
+            pb[n] = place(half * 8 + (j >> 2), bn + n * 32 + grp * 16 + (j & 3u) * 4, BN);
+        s16x8 a[2][TM], b[2][TN];
+        auto read = [&](int f, uint32_t buf, int kk) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.0f;
+            for (int m = 0; m < TM; ++m) {
+                const s16x4 lo = read_tr(&sa[buf][pa[m] + kk * 16 * BM]);
+                const s16x4 hi = read_tr(&sa[buf][pa[m] + (kk * 16 + 4) * BM]);
+                a[f][m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+#pragma unroll
+            for (int n = 0; n < TN; ++n) {
+                const s16x4 lo = read_tr(&sb[buf][pb[n] + kk * 16 * BN]);
+                const s16x4 hi = read_tr(&sb[buf][pb[n] + (kk * 16 + 4) * BN]);
+                b[f][n] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+        };
 
-    auto multiply = [&](int f) {
+        f32x16 acc[TM][TN];
 #pragma unroll
         for (int m = 0; m < TM; ++m)
 #pragma unroll
-            for (int n = 0; n < TN; ++n) acc[m][n] = mfma<F>(a[f][m], b[f][n], acc[m][n]);
-    };
-
-    if (steps > 0) {
-        load(0);
-        stage_a(0);
-        stage_b(0);
-        if (steps > 1) load(1);
-        __syncthreads();
-        read(0, 0, 0);
-    }
-    // A step: fragments one MFMA step ahead; the next step's tiles go to LDS beside the
-    // first two MFMA steps, and the ones after that are requested from memory as their
-    // registers become free.  The barrier stands where every wave has this buffer's last
-    // fragments in registers and its share of the next buffer written: behind it the next
-    // buffer may be read and this one be overwritten.
-    //
-    // Steady state, free of branches so that each MFMA step is one scheduling region: a
-    // wave's LDS reads, conversions, LDS writes and requests are dealt between its MFMAs.
-    // (The checkpoint first, then dy: 952 us; the other way round 985 us.)
-    constexpr int kMfma = TM * TN, kReads = 2 * (TM + TN);
-    auto steady = [&](uint32_t s, uint32_t buf) {
-        static_assert(KK >= 4 && KK % 2 == 0, "staging takes two MFMA steps, fragments alternate");
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            if (kk + 1 == KK) __syncthreads();
-            read((kk + 1) & 1, kk + 1 == KK ? buf ^ 1u : buf, (kk + 1) % KK);
-            multiply(kk & 1);
-            if (kk == 0) {
-                stage_b(buf ^ 1u);
-                load_b(s + 2);
-                interleave<kMfma, kReads, 12 * PB, PB, 2 * PB>();
-            } else if (kk == 1) {
-                stage_a(buf ^ 1u);
-                load_a(s + 2);
-                interleave<kMfma, kReads, 0, PA, PA>();
-            } else {
-                interleave<kMfma, kReads, 0, 0, 0>();
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    auto step = [&](uint32_t s, uint32_t buf) {
-        const bool more = s + 1 < steps;
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            if (kk + 1 < KK) {
-                read((kk + 1) & 1, buf, kk + 1);
-            } else {
-                __syncthreads();
-                if (more) read(0, buf ^ 1u, 0);
-            }
-            if (kk == 0 && more) {
-                stage_a(buf ^ 1u);
-                stage_b(buf ^ 1u);
-                if (s + 2 < steps) load(s + 2);
-            }
-            multiply(kk & 1);
-        }
-    };
-    uint32_t s = 0;
-    for (; s + 4 < steps; s += 2) {   // steps s + 2 and s + 3 are whole
-        steady(s, 0);
-        steady(s + 1, 1);
-    }
-    for (; s < steps; ++s) step(s, s & 1u);
-
-    // the lane again, opaque: what the stores need is worked out here and not kept in
-    // registers (or spilled) from before the loop
-    uint32_t el = lane;
-    asm volatile("" : "+v"(el));
-    const uint32_t eh = el >> 5;
-    // result register r of a lane: row 8 (r/4) + 4 half + r%4, column lane mod 32;
-    // positions of the last group stand for the row's last eight columns
-    auto column = [](uint32_t at, uint32_t first, uint32_t n) {   // ~0: not this one's to store
-        const uint32_t c = first + at;
-        if (TINY || first + (at | 7u) < n) return c < n ? c : ~0u;
-        const uint32_t group = c & ~7u;
-        if (group >= n) return ~0u;
-        const uint32_t real = n - 8 + (c & 7u);
-        return real >= group ? real : ~0u;
-    };
-    if constexpr (O == Out::k16 && !TINY) {
-        // Stored as they lie, a wave's 16-bit results are 64-B pieces of 128-B lines (1.8
-        // times the bytes moved, a tenth of the time at 2048 tokens).  Each wave turns 32
-        // rows at a time through LDS (its own part: every wave is past the last barrier,
-        // behind which nothing is read) into rows of 16-B groups.  Units of 32 columns are
-        // swapped in every second four rows, so that the two halves of a wave write
-        // different banks.
-        constexpr uint32_t W = BN / WN, kPerRow = W / 8, kRows = 64 / kPerRow;
-        constexpr uint32_t kSwap = W >= 64 ? 32 : 0;
-        static_assert(WM * WN * 32 * W <= 2 * kStep * BM, "room for 32 rows a wave");
-        uint16_t *const mine = &sa[0][0] + wave * (32 * W);
-        const uint32_t c = el % kPerRow * 8, group = i0 + bn + c;
-#pragma unroll
-        for (int m = 0; m < TM; ++m) {
-#pragma unroll
             for (int n = 0; n < TN; ++n)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    mine[(8 * (r / 4) + 4 * eh + r % 4) * W +
-                         ((n * 32 + (el & 31u)) ^ (eh * kSwap))] = from_f32<F>(acc[m][n][r]);
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            for (uint32_t r0 = 0; r0 < 32; r0 += kRows) {
-                const uint32_t r = r0 + el / kPerRow;
-                const uint32_t row = column(am + m * 32 + r, o0, g.n_out);
-                if (row == ~0u || group >= g.n_in) continue;
-                const uint16_t *v = &mine[r * W + (c ^ (((r >> 2) & 1u) * kSwap))];
-                uint16_t *d = static_cast<uint16_t *>(out) + static_cast<uint64_t>(row) * g.n_in;
-                if (group + 8 <= g.n_in) {
-                    *reinterpret_cast<u32x4_any *>(d + group) = *reinterpret_cast<const u32x4 *>(v);
-                } else {   // the row's last eight columns, those from `group` on
-                    for (uint32_t k = group - (g.n_in - 8); k < 8; ++k) d[g.n_in - 8 + k] = v[k];
-                }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+                for (int r = 0; r < 16; ++r) acc[m][n][r] = 0.0f;
+
+        auto multiply = [&](int f) {
+#pragma unroll
+            for (int m = 0; m < TM; ++m)
+#pragma unroll
+                for (int n = 0; n < TN; ++n) acc[m][n] = mfma<F>(a[f][m], b[f][n], acc[m][n]);
+        };
+
+        if (steps > 0) {
+            load(0);
+            stage_a(0);
+            stage_b(0);
+            if (steps > 1) load(1);
+            __syncthreads();
+            read(0, 0, 0);
         }
-        __syncthreads();   // the next tile writes LDS
-        continue;
-    }
-    const uint64_t plane = static_cast<uint64_t>(g.n_out) * g.n_in;
+        // A step: fragments one MFMA step ahead; the next step's tiles go to LDS beside the
+        // first two MFMA steps, and the ones after that are requested from memory as their
+        // registers become free.  The barrier stands where every wave has this buffer's last
+        // fragments in registers and its share of the next buffer written: behind it the next
+        // buffer may be read and this one be overwritten.
+        //
+        // Steady state, free of branches so that each MFMA step is one scheduling region: a
+        // wave's LDS reads, conversions, LDS writes and requests are dealt between its MFMAs.
+        // (The checkpoint first, then dy: 952 us; the other way round 985 us.)
+        constexpr int kMfma = TM * TN, kReads = 2 * (TM + TN);
+        auto steady = [&](uint32_t s, uint32_t buf) {
+            static_assert(KK >= 4 && KK % 2 == 0,
+                          "staging takes two MFMA steps, fragments alternate");
 #pragma unroll
-    for (int n = 0; n < TN; ++n) {
-        const uint32_t col = column(bn + n * 32 + (el & 31u), i0, g.n_in);
-#pragma unroll
-        for (int m = 0; m < TM; ++m) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
+            for (int kk = 0; kk < KK; ++kk) {
+                if (kk + 1 == KK) __syncthreads();
+                read((kk + 1) & 1, kk + 1 == KK ? buf ^ 1u : buf, (kk + 1) % KK);
+                multiply(kk & 1);
+                if (kk == 0) {
+                    stage_b(buf ^ 1u);
+                    load_b(s + 2);
+                    interleave<kMfma, kReads, 12 * PB, PB, 2 * PB>();
+                } else if (kk == 1) {
+                    stage_a(buf ^ 1u);
+                    load_a(s + 2);
+                    interleave<kMfma, kReads, 0, PA, PA>();
+                } else {
+                    interleave<kMfma, kReads, 0, 0, 0>();
+                }
                 __builtin_amdgcn_sched_barrier(0);
-                const uint32_t row = column(am + m * 32 + 8 * (r / 4) + 4 * eh + r % 4, o0,
-                                            g.n_out);
-                if (row != ~0u && col != ~0u) {
-                    const uint64_t at = static_cast<uint64_t>(row) * g.n_in + col;
-                    if constexpr (O == Out::k16) {
-                        static_cast<uint16_t *>(out)[at] = from_f32<F>(acc[m][n][r]);
-                    } else {
-                        float *d = static_cast<float *>(out) + blockIdx.y * plane + at;
-                        *d = O == Out::kAdd32 ? *d + acc[m][n][r] : acc[m][n][r];
+            }
+        };
+        auto step = [&](uint32_t s, uint32_t buf) {
+            const bool more = s + 1 < steps;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                if (kk + 1 < KK) {
+                    read((kk + 1) & 1, buf, kk + 1);
+                } else {
+                    __syncthreads();
+                    if (more) read(0, buf ^ 1u, 0);
+                }
+                if (kk == 0 && more) {
+                    stage_a(buf ^ 1u);
+                    stage_b(buf ^ 1u);
+                    if (s + 2 < steps) load(s + 2);
+                }
+                multiply(kk & 1);
+            }
+        };
+        uint32_t s = 0;
+        for (; s + 4 < steps; s += 2) {   // steps s + 2 and s + 3 are whole
+            steady(s, 0);
+            steady(s + 1, 1);
+        }
+        for (; s < steps; ++s) step(s, s & 1u);
+
+        // the lane again, opaque: what the stores need is worked out here and not kept in
+        // registers (or spilled) from before the loop
+        uint32_t el = lane;
+        asm volatile("" : "+v"(el));
+        const uint32_t eh = el >> 5;
+        // result register r of a lane: row 8 (r/4) + 4 half + r%4, column lane mod 32;
+        // positions of the last group stand for the row's last eight columns
+        auto column = [](uint32_t at, uint32_t first, uint32_t n) {   // ~0: not this one's to store
+            const uint32_t c = first + at;
+            if (TINY || first + (at | 7u) < n) return c < n ? c : ~0u;
+            const uint32_t group = c & ~7u;
+            if (group >= n) return ~0u;
+            const uint32_t real = n - 8 + (c & 7u);
+            return real >= group ? real : ~0u;
+        };
+        if constexpr (O == Out::k16 && !TINY) {
+            // Stored as they lie, a wave's 16-bit results are 64-B pieces of 128-B lines (1.8
+            // times the bytes moved, a tenth of the time at 2048 tokens).  Each wave turns 32
+            // rows at a time through LDS (its own part: every wave is past the last barrier,
+            // behind which nothing is read) into rows of 16-B groups.  Units of 32 columns are
+            // swapped in every second four rows, so that the two halves of a wave write
+            // different banks.
+            constexpr uint32_t W = BN / WN, kPerRow = W / 8, kRows = 64 / kPerRow;
+            constexpr uint32_t kSwap = W >= 64 ? 32 : 0;
+            static_assert(WM * WN * 32 * W <= 2 * kStep * BM, "room for 32 rows a wave");
+            uint16_t *const mine = &sa[0][0] + wave * (32 * W);
+            const uint32_t c = el % kPerRow * 8, group = i0 + bn + c;
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+#pragma unroll
+                for (int n = 0; n < TN; ++n)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        mine[(8 * (r / 4) + 4 * eh + r % 4) * W +
+                             ((n * 32 + (el & 31u)) ^ (eh * kSwap))] = from_f32<F>(acc[m][n][r]);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                for (uint32_t r0 = 0; r0 < 32; r0 += kRows) {
+                    const uint32_t r = r0 + el / kPerRow;
+                    const uint32_t row = column(am + m * 32 + r, o0, g.n_out);
+                    if (row == ~0u || group >= g.n_in) continue;
+                    const uint16_t *v = &mine[r * W + (c ^ (((r >> 2) & 1u) * kSwap))];
+                    uint16_t *d =
+                        static_cast<uint16_t *>(out) + static_cast<uint64_t>(row) * g.n_in;
+                    if (group + 8 <= g.n_in) {
+                        *reinterpret_cast<u32x4_any *>(d + group) =
+                            *reinterpret_cast<const u32x4 *>(v);
+                    } else {   // the row's last eight columns, those from `group` on
+                        for (uint32_t k = group - (g.n_in - 8); k < 8; ++k)
+                            d[g.n_in - 8 + k] = v[k];
+                    }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
+            __syncthreads();   // the next tile writes LDS
+            continue;
+        }
+        const uint64_t plane = static_cast<uint64_t>(g.n_out) * g.n_in;
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+            const uint32_t col = column(bn + n * 32 + (el & 31u), i0, g.n_in);
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    const uint32_t row = column(am + m * 32 + 8 * (r / 4) + 4 * eh + r % 4, o0,
+                                                g.n_out);
+                    if (row != ~0u && col != ~0u) {
+                        const uint64_t at = static_cast<uint64_t>(row) * g.n_in + col;
+                        if constexpr (O == Out::k16) {
+                            static_cast<uint16_t *>(out)[at] = from_f32<F>(acc[m][n][r]);
+                        } else {
+                            float *d = static_cast<float *>(out) + blockIdx.y * plane + at;
+                            *d = O == Out::kAdd32 ? *d + acc[m][n][r] : acc[m][n][r];
+                        }
                     }
                 }
             }
         }
-    }
-    __syncthreads();   // the next tile writes LDS
+        __syncthreads();   // the next tile writes LDS
     }
 }
 
