@@ -75,7 +75,7 @@ def check(got, z, a, old, ref, adv, w, kl, S, dt, what=""):
 SHAPES = [(1, 1), (3, 2), (5, 7), (4, 8), (6, 9), (9, 511), (7, 1024), (3, 1025), (5, 2047),
           (4, 4096), (3, 8193), (2, 16385), (3, 32771), (2, 50257), (2, 65537), (2, 131072),
           (2, 131073), (1, 200_003), (40, 300), (130, 65), (3, 49_153), (2, 98_305), (1, 262_144),
-          (2, 262_161), (1, 300_007)]
+          (2, 262_161), (1, 300_007), (2, 102_400), (2, 102_409), (3, 51_200), (3, 51_205)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
