@@ -42,6 +42,17 @@ def _parts(x, kind):
     return t, np.clip(x * dt, -1e6, 1e6), e / (1 + e), 1 / (1 + e)
 
 
+def value(x, kind, dt):
+    """(act(x), bound before the rounding to dt)."""
+    t, _, q, _ = _parts(x, kind)
+    y = np.where(t > 0, x - x * q, x * q)
+    if dt == "f32":
+        b = (np.abs(x * q) * (7 * np.abs(t) + 4) + np.where(t > 0, 0.0, np.abs(y))) * U * 1.01
+        return y, np.where(q > 0, b, 0.0) + 2.0 ** -138
+    live = np.abs(t) < 200
+    return y, np.where(live, np.abs(y) * (9 * np.abs(t) + 8) * U, 0.0) + 2.0 ** -117
+
+
 def slope(x, kind, dt):
     """(act'(x), bound before the product with dy and the rounding to dt)."""
     t, xt, q, r = _parts(x, kind)
@@ -70,6 +81,9 @@ def evaluate(what, h, kind, dt):
     e = torch.empty((h.shape[0], -(-h.shape[1] // 32)), dtype=torch.uint8, device=DEV)
     out = torch.empty_like(x)
     zs.zero_act_save(q, e, x, act=ACTS[kind], y=out)
+    if what == "forward":
+        v = plain.f64(h)
+        return (plain.f64(out), *value(v, kind, dt), v)
     zs.zero_act_backward(out, torch.ones_like(x), q, e, ACTS[kind])
     v = plain.decode(q.cpu().numpy(), e.cpu().numpy())
     return (plain.f64(out), *slope(v, kind, dt), v)
@@ -82,7 +96,7 @@ MAGNITUDES = [1e-40, 2.0 ** -126, 1e-20, 0.75, 12.0, 16.0, 20.0, 44.0, 64.0, 80.
 
 @pytest.mark.parametrize("kind", ["gelu", "silu"])
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("what", ["slope"])
+@pytest.mark.parametrize("what", ["forward", "slope"])
 def test_far_inputs(what, dt, kind):
     # each alone in its block, of both signs, so that its checkpoint is within 2^-4 of it
     m = [v for v in MAGNITUDES if v < (6.2e4 if dt == "f16" else 3.1e38)] + [plain.TOP[dt]]
@@ -98,7 +112,7 @@ def test_far_inputs(what, dt, kind):
 
 
 @pytest.mark.parametrize("kind", ["gelu", "silu"])
-@pytest.mark.parametrize("what", ["slope"])
+@pytest.mark.parametrize("what", ["forward", "slope"])
 def test_fp32_to_the_last_bits(what, kind):
     g = torch.Generator().manual_seed(21)
     got, want, bound, _ = evaluate(what, torch.randn(1024, 1024, generator=g) * 2, kind, "f32")
@@ -109,7 +123,7 @@ def test_fp32_to_the_last_bits(what, kind):
 
 
 @pytest.mark.parametrize("kind", ["gelu", "silu"])
-@pytest.mark.parametrize("what", ["slope"])
+@pytest.mark.parametrize("what", ["forward", "slope"])
 def test_fp32_no_further_off_than_the_elementary_form(what, kind):
     # error over 2^20 normal values against 64 bits, next to the formulas in elementary FP32
     # operations: the form by e^-|t| has the fewer roundings where the results are large
@@ -125,3 +139,14 @@ def test_fp32_no_further_off_than_the_elementary_form(what, kind):
             0.5 * (1 + t) + 0.5 * x * (1 - t * t) * c * (1 + 3 * a * x * x)
     ours, theirs = np.linalg.norm(got - want), np.linalg.norm(plain.f64(form) - want)
     assert ours <= theirs
+
+
+def test_infinite_inputs_of_the_forward_pass():
+    for dt in ("f16", "bf16", "f32"):
+        for kind in ("gelu", "silu"):
+            h = torch.zeros(1, 64, dtype=plain.TORCH[dt])
+            h[0, 3], h[0, 40], h[0, 41] = float("inf"), float("nan"), 100.0
+            with np.errstate(invalid="ignore"):
+                y = evaluate("forward", h, kind, dt)[0]
+            assert y[0, 3] == np.inf and np.isnan(y[0, 40]) and y[0, 41] == 100.0
+            assert np.isfinite(np.delete(y[0], [3, 40])).all()

@@ -52,10 +52,11 @@ struct Group {
 // Activation functions, act(x) = x s(t) with s(t) = 1 / (1 + e^-t).
 //
 // FP32 data: with e = e^-|t|, q = e / (1 + e) = s(-|t|) and r = 1 / (1 + e) = s(|t|),
+//     act(x)  = x - x q  for t > 0,  x q  otherwise
 //     act'(x) = 1 + q (x t' r - 1)  for t > 0,  q (x t' r + 1)  otherwise.
 // e never overflows and reaches zero with t on both sides (e^-t held at the range's end left
 // a slope of x 2^-125), and where the result is large the evaluation's error is scaled by the
-// small q: one rounding remains.  16384 x 8192 FP32: GELU backward 226 us.
+// small q: one rounding remains.  16384 x 8192 FP32: GELU forward 224 us, backward 226 us.
 //
 // For 16-bit data the constants are folded into one polynomial, e^-t = 2^(x (a + b x^2)),
 // and the hardware's 2^x and reciprocal (each within an ulp, zero for subnormals, which
@@ -85,10 +86,15 @@ __device__ __forceinline__ float exp_neg_t(float x) {
 
 template <int F, int ACT>
 __device__ __forceinline__ float act_value(float x) {
-    if constexpr (F == 2)
-        return x * (1.0f / (1.0f + expf(-inner<ACT>(x))));
-    else
+    if constexpr (F == 2) {
+        const float t = inner<ACT>(x), e = expf(-__builtin_fabsf(t));
+        const float q = e / (1.0f + e);
+        // the factor of q held at the largest number, so that infinity less nothing is infinity
+        const float h = x < 0x1.fffffep127f ? x : 0x1.fffffep127f;
+        return t > 0.0f ? __builtin_fmaf(-h, q, x) : x * q;
+    } else {
         return x * __builtin_amdgcn_rcpf(1.0f + exp_neg_t<ACT>(x));
+    }
 }
 
 // act'(x).  Past |x| = 20 the GELU's slope is 0 or 1; t' is taken from x held there, which
