@@ -211,19 +211,27 @@ struct RowGrad {
     float hit;      // S w g, added at the target
 };
 
-// e^d - 1: its series up to |d| = 1 (the first term left out is below 2^-28 of the
-// sum), the difference beyond, where it cancels no more than one bit.  Written out
-// because it is live beside the whole row: the library's form would push logits out
-// of registers.
-__device__ __forceinline__ float exp_minus_1(float d) {
-    if (!(__builtin_fabsf(d) <= 1.0f)) return exp_fast(d) - 1.0f;
+// e^d - 1 - d and e^d - 1.  Up to |d| = 1 the first by its own series (the first term left
+// out is below 2^-31 of the sum), and the second as d more: a difference of the two would
+// lose d's digits twice as the policy comes near its reference (all of them at d = 1e-6).
+// Beyond, differences, which cancel no more than two bits.  Written out because it is live
+// beside the whole row: the library's form would push logits out of registers.
+struct ExpTail {
+    float tail, minus_1;
+};
+__device__ __forceinline__ ExpTail exp_tail(float d) {
+    if (!(__builtin_fabsf(d) <= 1.0f)) {
+        const float em = exp_fast(d) - 1.0f;
+        return ExpTail{em - d, em};
+    }
     float s = 1.0f;
 #pragma unroll
-    for (int n = 12; n >= 2; --n) s = __builtin_fmaf(d * (1.0f / n), s, 1.0f);
-    return d * s;
+    for (int n = 12; n >= 3; --n) s = __builtin_fmaf(d * (1.0f / n), s, 1.0f);
+    const float t = d * d * 0.5f * s;
+    return ExpTail{t, d + t};
 }
 __device__ __forceinline__ float exp_near(float x) {
-    return __builtin_fabsf(x) <= 1.0f ? 1.0f + exp_minus_1(x) : exp_fast(x);
+    return __builtin_fabsf(x) <= 1.0f ? 1.0f + exp_tail(x).minus_1 : exp_fast(x);
 }
 
 // ln(x) for x of normal FP32 range, to about 2^-25 absolute next to the exact multiple
@@ -274,9 +282,9 @@ __device__ __forceinline__ RowGrad finish_row(const PolicyArgs &a, RowIn in, uin
     float g = cut ? 0.0f : p0;
     if (a.ref_logp != nullptr && a.kl_coef != 0.0f) {
         const float d = static_cast<float>(static_cast<double>(in.ref_logp) - lp);
-        const float em = exp_minus_1(d);
-        L = L + a.kl_coef * (em - d);
-        g = g - a.kl_coef * em;
+        const ExpTail x = exp_tail(d);
+        L = L + a.kl_coef * x.tail;
+        g = g - a.kl_coef * x.minus_1;
     }
     if (lane == 0) {
         a.token_loss[t] = L;
