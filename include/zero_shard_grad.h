@@ -20,7 +20,9 @@
  *     flat buffer.
  *   - Matrices of one call may not overlap, except where a function says so;
  *     overlaps are rejected with ZERO_EINVAL.  (Two matrices with the same row
- *     stride in bytes may interleave: columns [0, a) and [a, b) of one buffer.)
+ *     stride in bytes may interleave: columns [0, a) and [a, b) of one buffer.
+ *     Otherwise a matrix counts as all bytes from its first element to its
+ *     last, the gaps between its rows included.)
  *   - Extents (rows, columns, tokens, vocabulary, ...) are at most
  *     ZERO_MAX_EXTENT, and a matrix spans less than 2^56 bytes.
  *   - Results are repeatable bit for bit: every sum is taken in an order that
@@ -123,6 +125,8 @@ int zero_act_backward(void *dx, uint64_t lddx, const void *dy, uint64_t lddy, ze
  *        16-byte aligned; may be NULL if that is 0.  Its contents before the
  *        call do not matter.
  *   tokens == 0: dw = 0 when first, else no-op.  n_out or n_in == 0: no-op.
+ *   Row strides or n_in of 2^24 elements and more, and extents below 8, are
+ *   correct but several times slower.
  *   Errors: ZERO_EDTYPE for a dt that is not 16-bit or a dw_dt that is neither
  *   dt nor ZERO_F32; ZERO_EINVAL as above, for first == 0 with a 16-bit dw and
  *   for a small or misaligned workspace; ZERO_EHIP.
@@ -214,8 +218,8 @@ int zero_embed_grad_workspace(uint64_t tokens, uint64_t vocab, uint64_t width, u
  *   targets     device, rows ids of format it.
  *   old_logp, ref_logp  device FP32, rows values, or NULL.
  *   advantage, weight   device FP32, rows values.
- *   clip_low in [0, 1], clip_high >= 0 (infinity: no cut), kl_coef finite,
- *   loss_scale > 0 and finite.
+ *   clip_low in [0, 1], clip_high >= 0 (infinity: no cut), kl_coef finite (0:
+ *   ref_logp has no effect, whatever it holds), loss_scale > 0 and finite.
  *   rows == 0: loss = 0.
  *   Errors: ZERO_EDTYPE for a bad dt or it; ZERO_EINVAL for vocab == 0 with
  *   rows > 0, a NULL ref_logp with kl_coef != 0, and as above; ZERO_EHIP.

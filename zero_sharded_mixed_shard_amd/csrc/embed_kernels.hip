@@ -15,9 +15,9 @@
 //      write the zero rows of ids that do not occur.
 //   3. the partial rows of each run that crosses chunks are added.
 // What has to move is dy once and dw once; partial rows add at most
-// 2 * 2 * 4 / (64 * 2) = 1/8 of dy.  65536 x 4096 BF16 into FP32, vocabulary 50257, 28%
-// of the positions one id: sums and zero rows 240 us (5.9 TB/s of dy and dw),
-// sorting 28, joining 20.
+// 2 * 2 * 4 / (64 * 2) = 1/8 of dy (1/2 where few tokens are walked 16 at a time).
+// 65536 x 4096 BF16 into FP32, vocabulary 50257, 28% of the positions one id: sums and zero
+// rows 240 us (5.7 TB/s of dy and dw), sorting 28, joining 20.
 //
 // Sorting: up to kRankTokens tokens, a token's place is the number of keys that
 // precede it, counted directly in one launch (T^2 compares of two VALU operations
