@@ -65,6 +65,17 @@ column stride, gradients at any offset of a flat buffer):
                      old_logp=None, ref_logp=None, clip_low, clip_high, kl_coef, loss_scale,
                      dlogits=None)
     zero_policy_loss_dev(..., ctl=ctl)                 # loss scale from the control block
+
+The operators around a block's linear layers (include/zero_shard_block.h):
+
+    zero_block_quant(q, e, x, square=False, qt=None, et=None)   # 8-bit codes, blocks of 128
+    zero_block_load(x, q, e, square=False)             # the values they stand for
+    zero_block_product(y, qa, ea, qb, eb, workspace=ws)         # y = a b^T of two of them
+    zero_block_product_workspace(m, n, k) -> bytes
+    zero_dropout(y, x, p, seed, offset=0, d_offset=None)        # its own backward pass
+    zero_residual_norm(u, h, stats, r, f, post=..., pre=..., gate=..., res_scale=..., p=...)
+    zero_residual_norm_backward(df, dr, dh, du, f, u, stats, ..., d_gate=..., workspace=ws)
+    zero_residual_norm_workspace(rows, cols) -> bytes
 """
 from ._binding import (  # noqa: F401
     LIB_PATH,
@@ -129,6 +140,20 @@ from ._grad import (  # noqa: F401
     zero_weight_grad,
     zero_weight_grad_workspace,
 )
+from ._block import (  # noqa: F401
+    BLOCK,
+    NORM_LAYER,
+    NORM_NONE,
+    NORM_RMS,
+    zero_block_load,
+    zero_block_product,
+    zero_block_product_workspace,
+    zero_block_quant,
+    zero_dropout,
+    zero_residual_norm,
+    zero_residual_norm_backward,
+    zero_residual_norm_workspace,
+)
 
 __all__ = [
     "Layout",
@@ -187,4 +212,16 @@ __all__ = [
     "zero_policy_loss_dev",
     "zero_weight_grad",
     "zero_weight_grad_workspace",
+    "BLOCK",
+    "NORM_LAYER",
+    "NORM_NONE",
+    "NORM_RMS",
+    "zero_block_load",
+    "zero_block_product",
+    "zero_block_product_workspace",
+    "zero_block_quant",
+    "zero_dropout",
+    "zero_residual_norm",
+    "zero_residual_norm_backward",
+    "zero_residual_norm_workspace",
 ]

@@ -29,12 +29,14 @@ LIB = os.path.join(PKG, "libzero_shard.so")
 # SHA-256 of each kernel's machine code, written beside the library by build()
 ISA_HASHES = os.path.join(PKG, "kernel_isa.sha256")
 KERNEL_SOURCES = ["shard_kernels.hip", "exchange_kernels.hip", "act_kernels.hip",
-                  "wgrad_kernels.hip", "embed_kernels.hip", "policy_kernels.hip"]
+                  "wgrad_kernels.hip", "embed_kernels.hip", "policy_kernels.hip",
+                  "quant_kernels.hip", "product_kernels.hip", "dropout_kernels.hip",
+                  "residual_kernels.hip"]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["layout.cpp", "scaler.cpp", "accounting.cpp", "checkpoint.cpp", "api.cpp",
-           "grad_api.cpp", *KERNEL_SOURCES]
+           "grad_api.cpp", "block_api.cpp", *KERNEL_SOURCES]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-ffp-contract=off",
           f"-I{INCLUDE}", f"-I{CSRC}"]
 DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -50,7 +52,7 @@ def _run(cmd):
 
 def build(verbose: bool = False) -> str:
     """Compile every source for gfx950 and link the shared library."""
-    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(max_workers=4) as pool:
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(max_workers=8) as pool:
         objs = [os.path.join(tmp, src + ".o") for src in SOURCES]
         # every source goes through the HIP driver (host files include the runtime API)
         cmds = [[HIPCC, "-x", "hip", *DEVICE, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
