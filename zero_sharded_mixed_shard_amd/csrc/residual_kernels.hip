@@ -11,6 +11,11 @@
 // kinds of norm: sum dh u^, sum dh, A = sum G f^ and B = sum G; the gate's is w1 A + b1 B, the
 // post norm's gate A and gate B.
 //
+// What bounds it: HBM, with the arithmetic close behind.  16384 x 8192, norms of the mean
+// square on both sides and a gate: BF16 with the stream in FP32 291 us forward and 477
+// backward (5.5 and 5.1 TB/s), all BF16 220 and 280 (4.9 and 5.8).  Rows walked over several
+// times in memory took 398 and 672.
+//
 // Sums of squares are taken around the mean (two passes over a row that is on chip); rows
 // whose sum leaves FP32's middle are summed again scaled by 2^-80.
 #include "block_device.h"
@@ -395,6 +400,515 @@ __global__ __launch_bounds__(kWideThreads) void wide_backward_kernel(
     }
 }
 
+// ---- rows that stay on chip ---------------------------------------------------------------
+//
+// A row is held by W waves, V groups of eight columns a lane.  Rows of up to 64 x 8 V columns
+// take one wave each (no barriers) and several waves a workgroup; longer ones a workgroup each.
+//
+// The next row's data is on its way while this one is worked on, each operand requested anew
+// as soon as its registers are free: what a row needs first is asked for half a row before
+// what it needs last, so the memory is never waited for with nothing in flight (all requests
+// at one point: 244 and 348 us forward and backward at 16384 x 8192 BF16).  So that the waits
+// are exact, rows are read without a branch: lanes without columns read the row's last eight,
+// and an operand that is not there is read from another one's place.
+
+constexpr int kRowWaves = 16;   // most waves of a workgroup
+
+// Eight columns of a row from col on, read without a branch: where the row ends inside or
+// before them, its last eight (the row has eight at least).
+template <int F>
+__device__ __forceinline__ Raw8<F> raw_group(const elem_t<F> *row, uint32_t col, uint32_t cols) {
+    return load8<F>(row + (col + 8 <= cols ? col : cols - 8));
+}
+
+// What was read as the row's last eight, moved down to the n (1 to 7) that are the lane's,
+// zeros above.
+template <int F>
+__device__ __forceinline__ void move_down(Raw8<F> &r, uint32_t n) {
+    constexpr int kWords = F == 2 ? 8 : 4;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = r.v[j / 4][j % 4];
+    const uint32_t by = 8 - n;   // elements
+    if constexpr (F != 2) {
+        if (by & 1u) {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j)
+                w[j] = w[j] >> 16 | (j + 1 < kWords ? w[j + 1] << 16 : 0u);
+        }
+    }
+#pragma unroll
+    for (int k = F == 2 ? 1 : 2; k < 8; k *= 2) {
+        const int words = F == 2 ? k : k / 2;
+        if (by & static_cast<uint32_t>(k)) {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) w[j] = j + words < kWords ? w[j + words] : 0u;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) r.v[j / 4][j % 4] = w[j];
+}
+
+// The n (0 to 8) columns of a group that are the lane's, zeros past them; ragged: the row's
+// length is no multiple of eight.
+template <int F>
+__device__ __forceinline__ void widen_some(Raw8<F> &r, bool ragged, uint32_t n, float out[8]) {
+    if (ragged) {
+        if (n - 1u < 7u) move_down<F>(r, n);
+    }
+    if (n != 0) {
+        widen8<F>(r, out);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = 0.0f;
+    }
+}
+
+// Sums over a row's W waves, the same in every lane.  The waves' sums go through LDS, in two
+// halves in turn, so that one barrier a sum is enough; W == 1 needs neither.
+struct RowTotal {
+    float (*slots)[2][kRowWaves];   // [turn][value][wave]
+    uint32_t waves, wave, lane, turn;
+    __device__ __forceinline__ RowTotal(float (*p)[2][kRowWaves], uint32_t w)
+        : slots(p), waves(w),
+          wave(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6))),
+          lane(threadIdx.x & 63u), turn(0) {}
+    __device__ __forceinline__ float join(uint32_t which) const {
+        float x = (lane & 15u) < waves ? slots[turn][which][lane & 15u] : 0.0f;
+#define ZS_STEP(C) \
+    x = x + from_bits(__builtin_amdgcn_update_dpp(0u, bits(x), C, 0xf, 0xf, true))
+        ZS_STEP(0xB1);
+        ZS_STEP(0x4E);
+        ZS_STEP(0x141);
+        ZS_STEP(0x140);
+#undef ZS_STEP
+        return x;
+    }
+    __device__ __forceinline__ float operator()(float x) {
+        x = wave_total(x);
+        if (waves == 1) return x;
+        turn ^= 1u;
+        if (lane == 0) slots[turn][0][wave] = x;
+        __syncthreads();
+        return join(0);
+    }
+    __device__ __forceinline__ void operator()(float *x, float *y) {
+        *x = wave_total(*x);
+        *y = wave_total(*y);
+        if (waves == 1) return;
+        turn ^= 1u;
+        if (lane == 0) {
+            slots[turn][0][wave] = *x;
+            slots[turn][1][wave] = *y;
+        }
+        __syncthreads();
+        *x = join(0);
+        *y = join(1);
+    }
+};
+
+// This lane's groups of a row: group v holds columns col(v) .. col(v) + n(v) - 1.
+template <int V>
+struct LaneColumns {
+    uint32_t at, step, cols;
+    __device__ __forceinline__ LaneColumns(uint32_t lane_of_row, uint32_t lanes, uint32_t c)
+        : at(lane_of_row * 8), step(lanes * 8), cols(c) {}
+    __device__ __forceinline__ uint32_t col(int v) const { return at + v * step; }
+    __device__ __forceinline__ uint32_t n(int v) const {
+        const uint32_t c = col(v);
+        return c >= cols ? 0u : cols - c < 8 ? cols - c : 8u;
+    }
+};
+
+// What the columns of a lane are multiplied with and shifted by: HELD in registers over all
+// its rows, or read again for each (where the registers do not suffice).  A parameter that is
+// not there costs nothing: the branch on it is the same in every lane.
+template <int F, int V, bool HELD>
+struct Held {
+    const void *p;
+    const void *q;         // nullable: a second factor
+    float other;
+    float v[HELD ? V : 1][8];
+    __device__ __forceinline__ Held(const void *first, const void *second, float o)
+        : p(first), q(second), other(o) {}
+    __device__ __forceinline__ bool there() const { return p != nullptr || q != nullptr; }
+    __device__ __forceinline__ void read(int i, uint32_t col, uint32_t n) {
+        load_param<F>(p, col, n, other, v[i]);
+        if (q == nullptr) return;
+        float w[8];
+        load_param<F>(q, col, n, 1.0f, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * w[j];
+    }
+    __device__ __forceinline__ void hold(const LaneColumns<V> &m) {
+        if constexpr (HELD) {
+            if (!there()) return;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (m.n(i) != 0) read(i, m.col(i), m.n(i));
+        }
+    }
+    // group i's eight values; only where there() is
+    __device__ __forceinline__ const float *at(const LaneColumns<V> &m, int i) {
+        if constexpr (HELD) return v[i];
+        read(0, m.col(i), m.n(i));
+        return v[0];
+    }
+};
+
+// waves: of a row (W).  A workgroup of W == 1 takes blockDim.x / 64 rows at once.
+template <int F, int R, int V>
+__global__ __launch_bounds__(64 * kRowWaves) void row_forward_kernel(
+    Step s, uint32_t waves, elem_t<R> *u, uint64_t ldu, elem_t<F> *h, uint64_t ldh, float *stats,
+    const elem_t<R> *r, uint64_t ldr, const elem_t<F> *f, uint64_t ldf) {
+    constexpr bool kHeld = V == 1;
+    __shared__ float slots[2][2][kRowWaves];
+    RowTotal total(slots, waves);
+    const MaskKey key(s.mask);
+    const float cols = static_cast<float>(s.cols);
+    const uint32_t at_once = waves == 1 ? blockDim.x >> 6 : 1u;
+    const LaneColumns<V> mine(waves == 1 ? total.lane : threadIdx.x, waves * 64, s.cols);
+    const uint64_t stride = static_cast<uint64_t>(gridDim.x) * at_once;
+    uint64_t row = static_cast<uint64_t>(blockIdx.x) * at_once + (waves == 1 ? total.wave : 0u);
+
+    const bool branch = f != nullptr, ragged = s.cols % 8 != 0;
+    const void *const at_f = branch ? static_cast<const void *>(f) : r;   // (only read)
+    Raw8<R> raw_r[V];
+    Raw8<F> raw_f[V];
+    auto fetch_r = [&](uint64_t t) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            raw_r[v] = raw_group<R>(r + t * ldr, mine.col(v), s.cols);
+    };
+    auto fetch_f = [&](uint64_t t) {
+        const auto *base = static_cast<const elem_t<F> *>(at_f) + (branch ? t * ldf : 0);
+#pragma unroll
+        for (int v = 0; v < V; ++v) raw_f[v] = raw_group<F>(base, mine.col(v), s.cols);
+    };
+    if (row < s.rows) {
+        fetch_f(row);
+        fetch_r(row);
+    }
+    Held<F, V, kHeld> w1(s.w1 != nullptr ? s.w1 : s.gate, s.w1 != nullptr ? s.gate : nullptr, 1.0f);
+    Held<F, V, kHeld> b1(s.b1, s.b1 != nullptr ? s.gate : nullptr, 0.0f);
+    Held<F, V, kHeld> w2(s.w2, nullptr, 1.0f), b2(s.b2, nullptr, 0.0f);
+    w1.hold(mine);
+    b1.hold(mine);
+    w2.hold(mine);
+    b2.hold(mine);
+    for (; row < s.rows; row += stride) {
+        const uint64_t next = row + stride < s.rows ? row + stride : row;
+        float x[V][8], b[V][8];
+#pragma unroll
+        for (int v = 0; v < V; ++v) widen_some<F>(raw_f[v], ragged, mine.n(v), b[v]);
+        fetch_f(next);
+        // the sum of op over the row of the values y
+        auto total_of = [&](float (*y)[8], auto &&op) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t n = mine.n(v);
+                if (n == 8) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum = sum + op(y[v][j]);
+                } else if (n != 0) {
+#pragma unroll
+                    for (uint32_t j = 0; j < 7; ++j) sum = sum + (j < n ? op(y[v][j]) : 0.0f);
+                }
+            }
+            return total(sum);
+        };
+        float mean1 = 0.0f, rho1 = 1.0f, mean2 = 0.0f, rho2 = 1.0f;
+        if (s.post != ZERO_NORM_NONE)
+            row_stats(s.post, cols, s.eps, [&](auto &&op) { return total_of(b, op); }, &mean1,
+                      &rho1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) widen_some<R>(raw_r[v], ragged, mine.n(v), x[v]);
+        fetch_r(next);
+        if (branch) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t n = mine.n(v);
+                if (n == 0) continue;
+                if (s.post == ZERO_NORM_LAYER) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) b[v][j] = b[v][j] - mean1;
+                }
+                if (s.post != ZERO_NORM_NONE) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) b[v][j] = b[v][j] * rho1;
+                }
+                if (w1.there()) {
+                    const float *w = w1.at(mine, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) b[v][j] = b[v][j] * w[j];
+                }
+                if (b1.there()) {
+                    const float *c = b1.at(mine, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) b[v][j] = b[v][j] + c[j];
+                }
+                if (s.mask.threshold != 0) {
+                    const uint32_t keep =
+                        key.keep8(static_cast<uint32_t>(row), mine.col(v) >> 3);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        b[v][j] = (keep >> j) & 1u ? b[v][j] * s.mask.factor : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[v][j] = __builtin_fmaf(s.res_scale, x[v][j], b[v][j]);
+                store_row<R>(u + row * ldu, mine.col(v), n, x[v]);
+            }
+        }
+        if (s.pre != ZERO_NORM_NONE) {
+            row_stats(s.pre, cols, s.eps, [&](auto &&op) { return total_of(x, op); }, &mean2,
+                      &rho2);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t n = mine.n(v);
+                if (n == 0) continue;
+                if (s.pre == ZERO_NORM_LAYER) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[v][j] = x[v][j] - mean2;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[v][j] = x[v][j] * rho2;
+                if (w2.there()) {
+                    const float *w = w2.at(mine, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[v][j] = product32(x[v][j], w[j]);
+                }
+                if (b2.there()) {
+                    const float *c = b2.at(mine, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[v][j] = x[v][j] + c[j];
+                }
+                store_row<F>(h + row * ldh, mine.col(v), n, x[v]);
+            }
+        }
+        if (stats != nullptr && mine.at == 0)
+            *reinterpret_cast<u32x4_any *>(stats + row * 4) =
+                u32x4{bits(mean1), bits(rho1), bits(mean2), bits(rho2)};
+    }
+}
+
+// Rows part * at_once + wave, further on by parts * at_once; the sums of a part's rows to
+// part[part][4][cols].  BIAS: the two sums that biases need as well.
+template <int F, int R, int V, int WAVES, bool BIAS>
+__global__ __launch_bounds__(64 * WAVES) void row_backward_kernel(
+    Step s, uint32_t waves, Back<F, R> p, float *__restrict__ part, uint32_t parts) {
+    constexpr bool kHeld = true;
+    __shared__ float slots[2][2][kRowWaves];
+    extern __shared__ float joined[];   // [rows at once][cols], W == 1 only
+    RowTotal total(slots, waves);
+    const MaskKey key(s.mask);
+    const float cols = static_cast<float>(s.cols);
+    const uint32_t at_once = waves == 1 ? blockDim.x >> 6 : 1u;
+    const LaneColumns<V> mine(waves == 1 ? total.lane : threadIdx.x, waves * 64, s.cols);
+    const uint64_t stride = static_cast<uint64_t>(parts) * at_once;
+    const bool pre = s.pre != ZERO_NORM_NONE, post = s.post != ZERO_NORM_NONE;
+    const bool ragged = s.cols % 8 != 0;
+    const bool layer1 = s.post == ZERO_NORM_LAYER, layer2 = s.pre == ZERO_NORM_LAYER;
+    Held<F, V, kHeld> w1(s.w1 != nullptr ? s.w1 : s.gate, s.w1 != nullptr ? s.gate : nullptr, 1.0f);
+    Held<F, V, kHeld> w2(s.w2, nullptr, 1.0f);
+    w1.hold(mine);
+    w2.hold(mine);
+    for (uint32_t q = blockIdx.x; q < parts; q += gridDim.x) {
+        uint64_t row = static_cast<uint64_t>(q) * at_once + (waves == 1 ? total.wave : 0u);
+        float sums[BIAS ? 4 : 2][V][8] = {};
+        Raw8<F> raw_dh[V], raw_f[V];
+        Raw8<R> raw_u[V], raw_du[V];
+        auto fetch_pre = [&](uint64_t t) {
+            const elem_t<F> *a = pre ? p.dh + t * p.lddh : p.f + t * p.ldf;
+            const elem_t<R> *b = pre ? p.u + t * p.ldu : p.du + t * p.lddu;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                raw_dh[v] = raw_group<F>(a, mine.col(v), s.cols);
+                raw_u[v] = raw_group<R>(b, mine.col(v), s.cols);
+            }
+        };
+        auto fetch_post = [&](uint64_t t) {
+            const elem_t<F> *a = p.f != nullptr ? p.f + t * p.ldf : p.dh + t * p.lddh;
+            const elem_t<R> *b = p.du != nullptr ? p.du + t * p.lddu : p.u + t * p.ldu;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                raw_f[v] = raw_group<F>(a, mine.col(v), s.cols);
+                raw_du[v] = raw_group<R>(b, mine.col(v), s.cols);
+            }
+        };
+        if (row < s.rows) {
+            fetch_pre(row);
+            fetch_post(row);
+        }
+        for (; row < s.rows; row += stride) {
+            const uint64_t next = row + stride < s.rows ? row + stride : row;
+            const float *st = p.stats + row * 4;
+            const float mean1 = st[0], rho1 = st[1], mean2 = st[2], rho2 = st[3];
+            // g: w2 dh; z: u^; columns past the row's end have zeros in g (G below), which
+            // keeps them out of every sum
+            float g[V][8], z[V][8], G[V][8], fh[V][8];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (!pre) continue;
+                widen_some<F>(raw_dh[v], ragged, mine.n(v), g[v]);
+                widen_some<R>(raw_u[v], ragged, mine.n(v), z[v]);
+            }
+            fetch_pre(next);
+            float zg2 = 0.0f, sg2 = 0.0f;
+            if (pre) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (mine.n(v) == 0) continue;
+                    if (layer2) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) z[v][j] = z[v][j] - mean2;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        z[v][j] = z[v][j] * rho2;
+                        sums[0][v][j] = __builtin_fmaf(g[v][j], z[v][j], sums[0][v][j]);
+                        if constexpr (BIAS) sums[1][v][j] = sums[1][v][j] + g[v][j];
+                    }
+                    if (w2.there()) {
+                        const float *w = w2.at(mine, v);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) g[v][j] = g[v][j] * w[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) zg2 = __builtin_fmaf(g[v][j], z[v][j], zg2);
+                    if (layer2) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sg2 = sg2 + g[v][j];
+                    }
+                }
+                if (layer2) {
+                    total(&zg2, &sg2);
+                    sg2 = sg2 / cols;
+                } else {
+                    zg2 = total(zg2);
+                }
+                zg2 = zg2 / cols;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                widen_some<F>(raw_f[v], ragged, mine.n(v), fh[v]);
+                widen_some<R>(raw_du[v], ragged, mine.n(v), G[v]);
+                if (p.du == nullptr) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) G[v][j] = 0.0f;
+                }
+            }
+            fetch_post(next);
+            if (pre) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        G[v][j] = __builtin_fmaf(
+                            rho2, __builtin_fmaf(-zg2, z[v][j], g[v][j] - sg2), G[v][j]);
+            }
+            float zg = 0.0f, sg = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t n = mine.n(v);
+                if (n == 0) continue;
+                float out[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) out[j] = product32(s.res_scale, G[v][j]);
+                store_row<R>(p.dr + row * p.lddr, mine.col(v), n, out);
+                if (p.f == nullptr) continue;
+                if (n != 8) {   // (g - sg is not zero there)
+#pragma unroll
+                    for (uint32_t j = 1; j < 8; ++j) G[v][j] = j < n ? G[v][j] : 0.0f;
+                }
+                if (s.mask.threshold != 0) {
+                    const uint32_t keep =
+                        key.keep8(static_cast<uint32_t>(row), mine.col(v) >> 3);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        G[v][j] = (keep >> j) & 1u ? G[v][j] * s.mask.factor : 0.0f;
+                }
+                if (layer1) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) fh[v][j] = fh[v][j] - mean1;
+                }
+                if (post) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) fh[v][j] = fh[v][j] * rho1;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    constexpr int kA = BIAS ? 2 : 1;
+                    sums[kA][v][j] = __builtin_fmaf(G[v][j], fh[v][j], sums[kA][v][j]);
+                    if constexpr (BIAS) sums[3][v][j] = sums[3][v][j] + G[v][j];
+                }
+                if (w1.there()) {
+                    const float *w = w1.at(mine, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) G[v][j] = product32(G[v][j], w[j]);
+                }
+                if (post) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) zg = __builtin_fmaf(G[v][j], fh[v][j], zg);
+                }
+                if (layer1) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sg = sg + G[v][j];
+                }
+            }
+            if (post) {
+                if (layer1) {
+                    total(&zg, &sg);
+                    sg = sg / cols;
+                } else {
+                    zg = total(zg);
+                }
+                zg = zg / cols;
+            }
+            if (p.f != nullptr) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const uint32_t n = mine.n(v);
+                    if (n == 0) continue;
+                    if (post) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            G[v][j] = product32(rho1,
+                                                __builtin_fmaf(-zg, fh[v][j], G[v][j] - sg));
+                    }
+                    store_row<F>(p.df + row * p.lddf, mine.col(v), n, G[v]);
+                }
+            }
+        }
+        // sum k of this part: of one wave's rows (W > 1: of the workgroup's), or of its waves'
+        // in their order
+#pragma unroll
+        for (int k = 0; k < (BIAS ? 4 : 2); ++k) {
+            float *d = part + (static_cast<uint64_t>(q) * 4 + (BIAS ? k : 2 * k)) * s.cols;
+            if (at_once == 1) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (mine.n(v) != 0) store_row<2>(d, mine.col(v), mine.n(v), sums[k][v]);
+                continue;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    if (j < mine.n(v))
+                        joined[total.wave * s.cols + mine.col(v) + j] = sums[k][v][j];
+            __syncthreads();
+            for (uint32_t c = threadIdx.x; c < s.cols; c += blockDim.x) {
+                float x = joined[c];
+                for (uint32_t w = 1; w < at_once; ++w) x = x + joined[w * s.cols + c];
+                d[c] = x;
+            }
+        }
+    }
+}
+
 // ---- the parameters' gradients -----------------------------------------------------------
 
 struct Grads {
@@ -415,11 +929,11 @@ __device__ __forceinline__ void put_grad(void *d, uint32_t col, float v, bool fi
 
 // The parts' four sums of a column, added in the parts' order by kJoinParts lanes (each its
 // share), those joined in order, and the gradients made from them.  G: the gradients' format.
-constexpr uint32_t kJoinCols = 16, kJoinParts = 16;
+constexpr uint32_t kJoinCols = 32, kJoinParts = 32;
 template <int F, int G>
 __global__ __launch_bounds__(kJoinCols *kJoinParts) void join_grads_kernel(
-    Grads g, const float *__restrict__ part, uint32_t parts, uint32_t cols, const void *w1,
-    const void *b1, const void *gate) {
+    Grads g, const float *__restrict__ part, uint32_t parts, uint32_t cols, bool bias_sums,
+    const void *w1, const void *b1, const void *gate) {
     __shared__ float slots[4][kJoinParts][kJoinCols];
     const uint32_t lane_col = threadIdx.x % kJoinCols, share = threadIdx.x / kJoinCols;
     const uint32_t per = (parts + kJoinParts - 1) / kJoinParts;
@@ -429,10 +943,12 @@ __global__ __launch_bounds__(kJoinCols *kJoinParts) void join_grads_kernel(
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (col < cols) {
             const uint32_t from = share * per, to = from + per < parts ? from + per : parts;
+#pragma unroll 4
             for (uint32_t k = from; k < to; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    sum[i] = sum[i] + part[(static_cast<uint64_t>(k) * 4 + i) * cols + col];
+                    if (bias_sums || i % 2 == 0)
+                        sum[i] = sum[i] + part[(static_cast<uint64_t>(k) * 4 + i) * cols + col];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) slots[i][share][lane_col] = sum[i];
@@ -467,20 +983,90 @@ uint32_t capped(uint64_t n) {
     return static_cast<uint32_t>(n < cap ? n : cap);
 }
 
-// Parts of the rows in the column sums: by the extents alone.
-constexpr uint64_t kParts = 256;
-uint64_t rows_per_part(uint64_t rows) { return (rows + kParts - 1) / kParts; }
-uint64_t parts_of(uint64_t rows) {
-    const uint64_t per = rows_per_part(rows);
-    return (rows + per - 1) / per;
+// How rows of these extents are held: by the extents alone, so that the workspace and the
+// order of the sums do not depend on the device.
+struct RowPlan {
+    int groups;         // V, 0: rows are too long to stay on chip
+    uint32_t waves;     // W
+    uint32_t at_once;   // rows a workgroup takes at once
+    uint32_t parts;     // workgroups that sum over rows
+};
+
+constexpr uint64_t kUnits = 256;   // compute units of the chip
+
+uint32_t waves_of(uint64_t cols, int groups) {
+    const uint64_t span = 512u * groups;
+    return static_cast<uint32_t>((cols + span - 1) / span);
+}
+
+// What a lane holds wants 256 registers rather than 128.
+template <int F, int R>
+constexpr bool roomy(bool bias_sums) {
+    return F == 2 || (R == 2 && bias_sums);
+}
+
+// The backward pass: rows of one wave up to 1024 columns, so that a workgroup joins eight
+// rows' sums before it writes them; up to 8192 columns rows of several waves, one group a lane
+// (16 waves of 128 registers), or two (`roomy`, 8 of 256) where more is held: the four sums
+// beside FP32 data (16384 x 8192: 770 us against 844; 16-bit data with two sums: 378 against
+// 348).  As many parts as fill the chip once.
+RowPlan backward_plan(uint64_t rows, uint64_t cols, bool roomy) {
+    const uint64_t per = (rows + kUnits - 1) / kUnits;
+    RowPlan p{0, 1, 1, static_cast<uint32_t>((rows + per - 1) / per)};
+    if (cols > 8192 || cols < 8) return p;
+    p.groups = cols > 512 && (cols <= 1024 || roomy) ? 2 : 1;
+    p.waves = waves_of(cols, p.groups);
+    if (p.waves == 1) p.at_once = static_cast<uint32_t>(rows < 8 ? rows : 8);
+    const uint64_t resident = (p.groups == 1 ? 16 : 8) / (p.waves * p.at_once);
+    const uint64_t most = kUnits * (resident > 1 ? resident : 1);
+    const uint64_t need = (rows + p.at_once - 1) / p.at_once;
+    p.parts = static_cast<uint32_t>(need < most ? need : most);
+    return p;
 }
 
 template <int F, int R>
 hipError_t forward_as(const ResidualArgs &a, hipStream_t stream) {
-    wide_forward_kernel<F, R><<<capped(a.rows), kWideThreads, 0, stream>>>(
-        step_of(a), static_cast<elem_t<R> *>(a.u_out), a.ldu, static_cast<elem_t<F> *>(a.h), a.ldh,
-        a.stats, static_cast<const elem_t<R> *>(a.r), a.ldr, static_cast<const elem_t<F> *>(a.f),
-        a.ldf);
+    const Step s = step_of(a);
+    auto *u = static_cast<elem_t<R> *>(a.u_out);
+    auto *h = static_cast<elem_t<F> *>(a.h);
+    const auto *r = static_cast<const elem_t<R> *>(a.r);
+    const auto *f = static_cast<const elem_t<F> *>(a.f);
+    if (a.cols > 16384 || a.cols < 8) {
+        wide_forward_kernel<F, R><<<capped(a.rows), kWideThreads, 0, stream>>>(
+            s, u, a.ldu, h, a.ldh, a.stats, r, a.ldr, f, a.ldf);
+        return hipGetLastError();
+    }
+    const int groups = a.cols <= 8192 ? 1 : 2;
+    const uint32_t waves = waves_of(a.cols, groups);
+    const uint64_t per = (a.rows + kUnits - 1) / kUnits;
+    const uint32_t at_once = waves == 1 ? static_cast<uint32_t>(per < 8 ? per : 8) : 1u;
+    const uint32_t threads = 64 * waves * at_once;
+    // workgroups that fill the chip once: 16 waves a compute unit (of 128 registers each)
+    const uint64_t resident = 16 / (waves * at_once);
+    const uint64_t need = (a.rows + at_once - 1) / at_once;
+    const uint64_t most = kUnits * (resident > 1 ? resident : 1);
+    const uint32_t grid = capped(need < most ? need : most);
+    if (groups == 1)
+        row_forward_kernel<F, R, 1><<<grid, threads, 0, stream>>>(
+            s, waves, u, a.ldu, h, a.ldh, a.stats, r, a.ldr, f, a.ldf);
+    else
+        row_forward_kernel<F, R, 2><<<grid, threads, 0, stream>>>(
+            s, waves, u, a.ldu, h, a.ldh, a.stats, r, a.ldr, f, a.ldf);
+    return hipGetLastError();
+}
+
+template <int F, int R, bool BIAS>
+hipError_t rows_backward(const Step &s, const RowPlan &plan, const Back<F, R> &p, float *part,
+                         hipStream_t stream) {
+    const uint32_t threads = 64 * plan.waves * plan.at_once, grid = capped(plan.parts);
+    const size_t lds = plan.at_once > 1 ? sizeof(float) * plan.at_once * s.cols : 0;
+    constexpr bool kRoomy = roomy<F, R>(BIAS);
+    if (plan.groups == 1)
+        row_backward_kernel<F, R, 1, kRoomy ? 8 : 16, BIAS><<<grid, threads, lds, stream>>>(
+            s, plan.waves, p, part, plan.parts);
+    else
+        row_backward_kernel<F, R, 2, 8, BIAS><<<grid, threads, lds, stream>>>(
+            s, plan.waves, p, part, plan.parts);
     return hipGetLastError();
 }
 
@@ -492,32 +1078,43 @@ hipError_t backward_as(const ResidualArgs &a, hipStream_t stream) {
                        static_cast<elem_t<F> *>(a.df), static_cast<elem_t<R> *>(a.dr),
                        a.lddh, a.ldf, a.lddu, a.ldu, a.lddf, a.lddr, a.stats};
     float *part = static_cast<float *>(a.workspace);
-    const uint64_t parts = parts_of(a.rows), per = rows_per_part(a.rows);
-    float *means = part + parts * 4 * a.cols;
-    wide_means_kernel<F, R><<<capped(a.rows), kWideThreads, 0, stream>>>(s, p, means);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 grid(capped((a.cols + kWideThreads * 8ull - 1) / (kWideThreads * 8ull)),
-                    static_cast<uint32_t>(parts));
-    wide_backward_kernel<F, R><<<grid, kWideThreads, 0, stream>>>(s, p, means, part, per);
-    e = hipGetLastError();
+    bool bias_sums = a.db1 != nullptr || a.db2 != nullptr ||
+                     (a.dgate != nullptr && a.b1 != nullptr);
+    const RowPlan plan = backward_plan(a.rows, a.cols, roomy<F, R>(bias_sums));
+    hipError_t e;
+    if (plan.groups == 0) {
+        bias_sums = true;
+        float *means = part + static_cast<uint64_t>(plan.parts) * 4 * a.cols;
+        wide_means_kernel<F, R><<<capped(a.rows), kWideThreads, 0, stream>>>(s, p, means);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const dim3 grid(capped((a.cols + kWideThreads * 8ull - 1) / (kWideThreads * 8ull)),
+                        plan.parts);
+        wide_backward_kernel<F, R><<<grid, kWideThreads, 0, stream>>>(
+            s, p, means, part, (a.rows + plan.parts - 1) / plan.parts);
+        e = hipGetLastError();
+    } else {
+        e = bias_sums ? rows_backward<F, R, true>(s, plan, p, part, stream)
+                      : rows_backward<F, R, false>(s, plan, p, part, stream);
+    }
     if (e != hipSuccess) return e;
     const Grads g{a.dw1, a.db1, a.dgate, a.dw2, a.db2, a.first};
     if (!a.dw1 && !a.db1 && !a.dgate && !a.dw2 && !a.db2) return hipSuccess;
     const uint32_t blocks = capped((a.cols + kJoinCols - 1) / kJoinCols);
     if (a.grad32)
         join_grads_kernel<F, 2><<<blocks, kJoinCols * kJoinParts, 0, stream>>>(
-            g, part, static_cast<uint32_t>(parts), a.cols, a.w1, a.b1, a.gate);
+            g, part, plan.parts, a.cols, bias_sums, a.w1, a.b1, a.gate);
     else
         join_grads_kernel<F, F><<<blocks, kJoinCols * kJoinParts, 0, stream>>>(
-            g, part, static_cast<uint32_t>(parts), a.cols, a.w1, a.b1, a.gate);
+            g, part, plan.parts, a.cols, bias_sums, a.w1, a.b1, a.gate);
     return hipGetLastError();
 }
 
 }  // namespace
 
 uint64_t residual_workspace(uint64_t rows, uint64_t cols) {
-    return (parts_of(rows) * cols + rows) * 16;
+    const RowPlan p = backward_plan(rows, cols, false), q = backward_plan(rows, cols, true);
+    return ((p.parts > q.parts ? p.parts : q.parts) * cols + (p.groups == 0 ? rows : 0)) * 16;
 }
 
 hipError_t launch_residual_forward(const ResidualArgs &a, hipStream_t stream) {
