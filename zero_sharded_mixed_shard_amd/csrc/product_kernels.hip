@@ -34,10 +34,19 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+__device__ __forceinline__ uint32_t uniform(uint32_t x) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(x)));
+}
+
 // A pointer `bytes` past one that is the same in every lane, the base in scalar registers.
+// (readfirstlane: what the compiler knows to be the same costs nothing, and of the rest it
+// loses sight in divisions and loops.)
 template <typename T>
 __device__ __forceinline__ const GLOBAL_AS T *at_offset(const T *base, uint32_t bytes) {
-    auto *b = (const GLOBAL_AS char *)(base);
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    const uint64_t u = uniform(static_cast<uint32_t>(p)) |
+                       static_cast<uint64_t>(uniform(static_cast<uint32_t>(p >> 32))) << 32;
+    auto *b = (const GLOBAL_AS char *)(u);
     asm("" : "+s"(b));
     return (const GLOBAL_AS T *)(b + bytes);
 }
@@ -57,6 +66,28 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t lo, uint32_t hi, float 
 // Of what a code stands for only 2^-133, the smallest, is lost.
 __device__ __forceinline__ float half_scale(uint32_t e) { return from_bits((e - 1u) << 23); }
 constexpr float kUnhalve = 4.0f;
+
+// Order of a scheduling region that holds M MFMAs, R LDS reads, W LDS writes and G memory
+// reads: each kind dealt evenly between the MFMAs.
+template <int I, int M, int R, int W, int G>
+__device__ __forceinline__ void deal() {
+    if constexpr (I < M) {
+        constexpr int kTo = I + 1;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr (R * kTo / M > R * I / M)
+            __builtin_amdgcn_sched_group_barrier(0x100, R * kTo / M - R * I / M, 0);
+        if constexpr (W * kTo / M > W * I / M)
+            __builtin_amdgcn_sched_group_barrier(0x200, W * kTo / M - W * I / M, 0);
+        if constexpr (G * kTo / M > G * I / M)
+            __builtin_amdgcn_sched_group_barrier(0x020, G * kTo / M - G * I / M, 0);
+        deal<I + 1, M, R, W, G>();
+    }
+}
+template <int M, int R, int W, int G>
+__device__ __forceinline__ void interleave() {
+    deal<0, M, R, W, G>();
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 constexpr uint32_t kStep = 128;   // columns a step
 
@@ -90,11 +121,15 @@ __device__ __forceinline__ bool tile_of(const ProductShape &s, uint64_t w, uint3
     return gi * group_m < s.tiles_m && *i < s.tiles_m && *j < s.tiles_n;
 }
 
-// One BM x BN tile of y (or, SPLIT, of a split's FP32 plane); WM x WN waves.  EIGHT: the 8-bit
-// instruction.  Rows past the matrix are read as its last one and not stored; columns past it
-// are zeros.  k >= 16, and a tile's rows span less than 4 GiB (the launcher checks both).
-template <int F, bool EIGHT, bool SPLIT, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(
+// BM x BN tiles of y (or, SPLIT, of a split's FP32 plane); WM x WN waves.  EIGHT: the 8-bit
+// instruction.  A32: a's blocks are of 32 columns.  RAGGED: the last step is short.  Rows past the matrix are read as its last
+// one and not stored; columns past it are zeros.  k >= 16, and a tile's rows span less than
+// 4 GiB (the launcher checks both).
+//
+// b's rows are the matrix instruction's rows and a's its columns, so that a lane holds four
+// neighbours of a row of y.
+template <int F, bool EIGHT, bool SPLIT, bool A32, bool RAGGED, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_kernel(
     void *__restrict__ y, const uint8_t *__restrict__ qa, const uint8_t *__restrict__ ea,
     const uint8_t *__restrict__ qb, const uint8_t *__restrict__ eb, ProductShape s) {
     constexpr int kLanes = 64 * WM * WN;
@@ -102,259 +137,403 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(
     constexpr int kRows = kLanes / 8;                     // rows a pass of staging
     constexpr int PA = BM / kRows, PB = BN / kRows;
     static_assert(kLanes >= BM && BN / WN <= 128, "exponents: a lane a row, a byte a wave");
+    static_assert(kRows % 16 == 0, "a lane's rows share its unit's place");
     __shared__ __align__(16) uint8_t sa[2][BM * kStep];
     __shared__ __align__(16) uint8_t sb[2][BN * kStep];
-    __shared__ uint32_t se[2][BM];
+    __shared__ uint32_t se[2][kLanes];   // (of the first BM rows; the rest is not read)
+    // CHAIN: a workgroup's tiles are one long run of steps: the next tile's first ones are
+    // requested, staged and read into registers as the last ones of this are multiplied, and
+    // its results are stored beside them, through LDS of their own.
+    constexpr bool CHAIN = BM == 256;
+    constexpr uint32_t kTurn = 32 * 128;   // bytes a wave turns at a time: 32 rows of a line
+    __shared__ __align__(16) uint8_t sc[CHAIN ? WM * WN * kTurn : 16];
 
-    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave =
+        static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
     const uint32_t half = lane >> 5, row32 = lane & 31u;
     const uint32_t am = wave % WM * (BM / WM), bn = wave / WM * (BN / WN);
-    for (uint64_t work = blockIdx.x; work < s.work; work += gridDim.x) {
-        uint32_t ti, tj;
-        if (!tile_of(s, work, &ti, &tj)) continue;
-        const uint32_t i0 = ti * BM, j0 = tj * BN;
-        const uint32_t n = static_cast<uint32_t>(s.n);
-        const uint32_t all = (s.k + kStep - 1) / kStep;
-        const uint32_t s0 = blockIdx.y * s.per_split;
-        const uint32_t s1 = s0 + s.per_split < all ? s0 + s.per_split : all;
-        const uint32_t whole = s.k / kStep;               // steps before the last, short one
-        const uint8_t *const base_a = qa + static_cast<uint64_t>(i0) * s.k;
-        const uint8_t *const base_b = qb + static_cast<uint64_t>(j0) * s.k;
-        const uint8_t *const base_e = ea + static_cast<uint64_t>(i0) * s.blocks_a;
+    const uint32_t n = static_cast<uint32_t>(s.n);
+    const uint32_t whole = s.k / kStep;               // steps before the last, short one
+    const uint32_t all = whole + (RAGGED ? 1 : 0);
+    const uint32_t s0 = blockIdx.y * s.per_split;
+    const uint32_t s1 = s0 + s.per_split < all ? s0 + s.per_split : all;
 
-        // staging: this lane's unit of 16 columns and its rows
-        const uint32_t unit = threadIdx.x & 7u, row0 = threadIdx.x >> 3;
-        uint32_t off_a[PA], off_b[PB];
+    // Staging: this lane's unit of 16 columns and its rows.  LDS places: rows that a lane
+    // visits are multiples of 16 apart, so that its unit's place in a row is the same in all of
+    // them and the rest are constant offsets.
+    const uint32_t unit = threadIdx.x & 7u, row0 = threadIdx.x >> 3;
+    const uint32_t put = row0 * kStep + ((unit ^ ((row0 >> 1) & 7u)) << 4);
+    uint32_t get[4];   // unit 4 kk + 2 x + half of a row, at 2 kk + x
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        get[c] = row32 * kStep + (((2u * c + half) ^ ((row32 >> 1) & 7u)) << 4);
+
+    struct Tile {
+        uint32_t i0, j0;
+    };
+    // the first place from `at` on that has a tile
+    auto seek = [&](uint64_t at, Tile *t) {
+        for (; at < s.work; at += gridDim.x) {
+            uint32_t ti, tj;
+            const bool found = tile_of(s, at, &ti, &tj);
+            if (!uniform(found)) continue;
+            t->i0 = uniform(ti) * BM;
+            t->j0 = uniform(tj) * BN;
+            break;
+        }
+        return at;
+    };
+
+    // what is requested: step `ask` of tile `from`
+    Tile from{0, 0};
+    uint32_t ask = s0;
+    uint32_t off_a[PA], off_b[PB], off_e = 0;
+    u32x4 xa[PA], xb[PB];
+    uint32_t xe = 0, xeb = 0;
+    auto aim = [&]() {
+        const uint32_t last_a = s.m - 1 - from.i0, last_b = n - 1 - from.j0;
 #pragma unroll
         for (int p = 0; p < PA; ++p) {
-            const uint32_t r = row0 + p * kRows, last = s.m - 1 - i0;
-            off_a[p] = (r < last ? r : last) * s.k + unit * 16;
+            const uint32_t r = row0 + p * kRows;
+            off_a[p] = (r < last_a ? r : last_a) * s.k + (RAGGED ? 0u : unit * 16);
         }
 #pragma unroll
         for (int p = 0; p < PB; ++p) {
-            const uint32_t r = row0 + p * kRows, last = n - 1 - j0;
-            off_b[p] = (r < last ? r : last) * s.k + unit * 16;
+            const uint32_t r = row0 + p * kRows;
+            off_b[p] = (r < last_b ? r : last_b) * s.k + (RAGGED ? 0u : unit * 16);
         }
-        const uint32_t erow = threadIdx.x < s.m - 1 - i0 ? threadIdx.x : s.m - 1 - i0;
-        const uint32_t off_e = erow * s.blocks_a;
-        const uint32_t jb = j0 + bn < n ? (j0 + bn) >> 7 : (n - 1) >> 7;
-        const uint8_t *const row_eb = eb + static_cast<uint64_t>(jb) * s.blocks_b;
-        u32x4 xa[PA], xb[PB];
-        uint32_t xe, xeb;
+        off_e = (threadIdx.x < last_a ? threadIdx.x : last_a) * s.blocks_a;
+    };
+    auto base_a = [&]() { return qa + static_cast<uint64_t>(uniform(from.i0)) * s.k; };
+    auto base_b = [&]() { return qb + static_cast<uint64_t>(uniform(from.j0)) * s.k; };
+    auto base_e = [&]() { return ea + static_cast<uint64_t>(uniform(from.i0)) * s.blocks_a; };
+    auto byte_b = [&](uint32_t st) {
+        const uint32_t j = uniform(from.j0) + bn;
+        return eb[static_cast<uint64_t>((j < n ? j : n - 1) >> 7) * s.blocks_b + st];
+    };
+    // A short step's unit that the row ends in or before is read as the row's last 16 columns
+    // (and moved down by trim() before it is staged), so that requests do not branch: what
+    // comes from two branches is waited for where they meet.
+    auto column = [&](uint32_t st) {
+        const uint32_t c = st * kStep + unit * 16;
+        return c + 16 <= s.k ? c : s.k - 16;
+    };
+    auto load_a = [&](uint32_t st) {
+        const uint8_t *const p0 =
+            base_a() + (RAGGED ? 0ull : static_cast<uint64_t>(uniform(st)) * kStep);
+        const uint32_t c = RAGGED ? column(st) : 0u;
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+            xa[p] = *(const GLOBAL_AS u32x4_any *)at_offset(p0, off_a[p] + c);
+    };
+    auto load_b = [&](uint32_t st) {
+        const uint8_t *const p0 =
+            base_b() + (RAGGED ? 0ull : static_cast<uint64_t>(uniform(st)) * kStep);
+        const uint32_t c = RAGGED ? column(st) : 0u;
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+            xb[p] = *(const GLOBAL_AS u32x4_any *)at_offset(p0, off_b[p] + c);
+    };
+    // exponents of step st: a row's four bytes (one for each 32 columns; a block of 128 has the
+    // same in all; past the row's end the last), and the byte of this wave's block of b
+    auto load_exponents = [&](uint32_t st) {
+        typedef uint32_t u32_any __attribute__((aligned(1)));
+        if constexpr (A32 && RAGGED) {
+            const uint8_t *const p0 = base_e();
+            const uint32_t last = s.blocks_a - 1, i = st * 4;
+            xe = *at_offset(p0 + (i < last ? i : last), off_e);
+#pragma unroll
+            for (uint32_t j = 1; j < 4; ++j)
+                xe |= static_cast<uint32_t>(*at_offset(p0 + (i + j < last ? i + j : last), off_e))
+                      << (8 * j);
+        } else if constexpr (A32) {
+            xe = *(const GLOBAL_AS u32_any *)at_offset(base_e() + uniform(st) * 4, off_e);
+        } else {
+            xe = *at_offset(base_e() + uniform(st), off_e) * 0x01010101u;
+        }
+        xeb = byte_b(uniform(st));
+    };
+    uint32_t held = 0;   // the step that the staging registers hold
+    auto load = [&](uint32_t st) {
+        load_a(st);
+        load_b(st);
+        load_exponents(st);
+        held = st;
+    };
+    // 16 columns moved down by `by`, zeros above
+    auto move_down = [](u32x4 v, uint32_t by) {
+        uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32;
+        uint64_t hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
+        if (by >= 16) {
+            lo = hi = 0;
+        } else if (by >= 8) {
+            lo = hi >> (8 * by - 64);
+            hi = 0;
+        } else if (by > 0) {
+            lo = lo >> (8 * by) | hi << (64 - 8 * by);
+            hi >>= 8 * by;
+        }
+        return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                     static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+    };
+    auto trim = [&]() {
+        if (!RAGGED || uniform(held) != whole) return;
+        const uint32_t by = whole * kStep + unit * 16 - column(whole);
+#pragma unroll
+        for (int p = 0; p < PA; ++p) xa[p] = move_down(xa[p], by);
+#pragma unroll
+        for (int p = 0; p < PB; ++p) xb[p] = move_down(xb[p], by);
+    };
+    auto stage_a = [&](uint32_t buf) {
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+            *reinterpret_cast<u32x4 *>(&sa[buf][put + p * (kRows * kStep)]) = xa[p];
+        se[buf][threadIdx.x] = xe;
+    };
+    auto stage_b = [&](uint32_t buf) {
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+            *reinterpret_cast<u32x4 *>(&sb[buf][put + p * (kRows * kStep)]) = xb[p];
+    };
 
-        // The unit of 16 columns from column c of a row on, where the row ends inside it or
-        // before it: the row's last 16 bytes, moved down, zeros above.
-        auto tail = [&](const uint8_t *base, uint32_t row_at, uint32_t c) {
-            u32x4 v{0u, 0u, 0u, 0u};
-            if (c < s.k) {
-                const uint32_t have = s.k - c < 16 ? s.k - c : 16u;
-                v = *(const GLOBAL_AS u32x4_any *)at_offset(base, row_at + c + have - 16);
-                uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32;
-                uint64_t hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
-                const uint32_t by = 8 * (16 - have);
-                if (by >= 64) {
-                    lo = hi >> (by - 64);
-                    hi = 0;
-                } else if (by > 0) {
-                    lo = lo >> by | hi << (64 - by);
-                    hi >>= by;
+    // One request further: the next step, or the next tile's first one; nothing is left: the
+    // last step again, which nothing reads.
+    uint64_t asked = 0;
+    auto advance = [&]() {
+        if (ask + 1 < s1) {
+            ++ask;
+        } else if constexpr (CHAIN) {
+            Tile t{0, 0};
+            const uint64_t at = seek(asked + gridDim.x, &t);
+            if (at < s.work) {
+                asked = at;
+                from = t;
+                ask = s0;
+                aim();
+            }
+        }
+    };
+
+    f32x16 acc[TM][TN];
+            // Fragments of MFMA step kk (64 columns), and their products
+            constexpr int H = TN / 2;
+            i32x8 a[2][TM], b[TN == 1 ? 2 : TN];
+            uint32_t wa[TM], wb = 127u;
+            auto fragment = [&](const uint8_t *t, int i, int kk) {
+                const u32x4 lo = *reinterpret_cast<const u32x4 *>(&t[get[2 * kk] + i * (32 * kStep)]);
+                const u32x4 hi =
+                    *reinterpret_cast<const u32x4 *>(&t[get[2 * kk + 1] + i * (32 * kStep)]);
+                i32x8 v;
+    #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = static_cast<int>(lo[j]);
+                    v[4 + j] = static_cast<int>(hi[j]);
                 }
-                v = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
-                          static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
-            }
-            return v;
-        };
-        auto load_whole = [&](uint32_t st) {
-            const uint8_t *const pa = base_a + static_cast<uint64_t>(st) * kStep;
-            const uint8_t *const pb = base_b + static_cast<uint64_t>(st) * kStep;
-#pragma unroll
-            for (int p = 0; p < PA; ++p)
-                xa[p] = *(const GLOBAL_AS u32x4_any *)at_offset(pa, off_a[p]);
-#pragma unroll
-            for (int p = 0; p < PB; ++p)
-                xb[p] = *(const GLOBAL_AS u32x4_any *)at_offset(pb, off_b[p]);
-        };
-        auto load_tail = [&](uint32_t st) {
-            const uint32_t c = st * kStep + unit * 16;
-#pragma unroll
-            for (int p = 0; p < PA; ++p) xa[p] = tail(base_a, off_a[p] - unit * 16, c);
-#pragma unroll
-            for (int p = 0; p < PB; ++p) xb[p] = tail(base_b, off_b[p] - unit * 16, c);
-        };
-        // exponents of step st: a row's four bytes (one for each 32 columns; a block of 128
-        // has the same in all), and the byte of this wave's block of b
-        auto load_exponents = [&](uint32_t st) {
-            if (s.shift_a == 7) {
-                xe = *at_offset(base_e + st, off_e) * 0x01010101u;
-            } else if (st * 4 + 4 <= s.blocks_a) {
-                typedef uint32_t u32_any __attribute__((aligned(1)));
-                xe = *(const GLOBAL_AS u32_any *)at_offset(base_e + st * 4, off_e);
-            } else {
-                xe = 0x7f7f7f7fu;
-                for (uint32_t j = 0; st * 4 + j < s.blocks_a; ++j)
-                    xe = (xe & ~(0xffu << (8 * j))) |
-                         static_cast<uint32_t>(*at_offset(base_e + st * 4 + j, off_e)) << (8 * j);
-            }
-            xeb = row_eb[st];
-        };
-        auto load = [&](uint32_t st) {
-            if (st < whole)
-                load_whole(st);
-            else
-                load_tail(st);
-            load_exponents(st);
-        };
-        auto place = [](uint32_t r, uint32_t c) { return r * kStep + ((c ^ ((r >> 1) & 7u)) << 4); };
-        auto stage = [&](uint32_t buf) {
-#pragma unroll
-            for (int p = 0; p < PA; ++p)
-                *reinterpret_cast<u32x4 *>(&sa[buf][place(row0 + p * kRows, unit)]) = xa[p];
-#pragma unroll
-            for (int p = 0; p < PB; ++p)
-                *reinterpret_cast<u32x4 *>(&sb[buf][place(row0 + p * kRows, unit)]) = xb[p];
-            if (kLanes == BM || threadIdx.x < BM) se[buf][threadIdx.x] = xe;
-        };
+                return v;
+            };
+            auto read_a = [&](int f, uint32_t buf, int kk) {
+    #pragma unroll
+                for (int i = 0; i < TM; ++i) a[f][i] = fragment(&sa[buf][am * kStep], i, kk);
+            };
+            auto read_b = [&](int from, int to, uint32_t buf, int kk) {
+    #pragma unroll
+                for (int j = from; j < to; ++j)
+                    b[TN == 1 ? kk : j] = fragment(&sb[buf][bn * kStep], j, kk);
+            };
+            auto read_exponents = [&](uint32_t buf) {
+    #pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    wa[i] = se[buf][am + i * 32 + row32] >> (EIGHT ? 8 * half : 0);
+            };
+            auto times = [&](auto KK, int from, int to) {
+                constexpr int kk = decltype(KK)::value;
+                if constexpr (EIGHT) {
+    #pragma unroll
+                    for (int j = from; j < to; ++j)
+    #pragma unroll
+                        for (int i = 0; i < TM; ++i)
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                                b[TN == 1 ? kk : j], a[kk][i], acc[i][j], 0, 0, 0,
+                                static_cast<int>(wb), kk * 2, static_cast<int>(wa[i]));
+                } else {
+                    const float scale_b = half_scale(wb);
+    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        bf16x8 d[TM];
+    #pragma unroll
+                        for (int i = 0; i < TM; ++i)
+                            d[i] = codes_to_bf16(static_cast<uint32_t>(a[kk][i][2 * q]),
+                                                 static_cast<uint32_t>(a[kk][i][2 * q + 1]),
+                                                 half_scale((wa[i] >> (8 * (kk * 2 + q / 2))) & 0xffu));
+    #pragma unroll
+                        for (int j = from; j < to; ++j) {
+                            const i32x8 &v = b[TN == 1 ? kk : j];
+                            const bf16x8 c = codes_to_bf16(static_cast<uint32_t>(v[2 * q]),
+                                                           static_cast<uint32_t>(v[2 * q + 1]),
+                                                           scale_b);
+    #pragma unroll
+                            for (int i = 0; i < TM; ++i)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c, d[i], acc[i][j],
+                                                                                    0, 0, 0);
+                        }
+                    }
+                }
+            };
+            constexpr std::integral_constant<int, 0> k0{};
+            constexpr std::integral_constant<int, 1> k1{};
 
-        f32x16 acc[TM][TN];
+    // A step.  Four scheduling regions, each half an MFMA step's products; a wave's LDS reads,
+    // LDS writes and requests are dealt between its MFMAs.  Fragments are a region ahead: those
+    // of b's first half and of a for the next MFMA step, those of b's second half as the first
+    // half is multiplied.  The barrier stands where every wave has this buffer's last fragments
+    // in registers and its share of the next buffer written.
+    constexpr int kMfma = EIGHT ? 1 : 4;   // instructions a product of 64 columns
+    constexpr int B1 = TN > 1 ? H : 1;
+    uint32_t eb_next = 127u, buf = 0;
+    auto begin = [&]() {
+        load(ask);
+        trim();
+        advance();
+        stage_a(0);
+        stage_b(0);
+        eb_next = xeb;
+        load(ask);
+        __syncthreads();
+        buf = 0;
+        read_exponents(0);
+        read_a(0, 0, 0);
+        read_b(0, B1, 0, 0);
+    };
+
+    Tile tile{0, 0};
+    uint64_t work = seek(blockIdx.x, &tile);
+    bool begun = false;
+    for (; work < s.work; work = seek(work + gridDim.x, &tile)) {
+        if (!CHAIN || !begun) {
+            begun = true;
+            asked = work;
+            from = tile;
+            ask = s0;
+            aim();
+            begin();
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-        uint32_t wa[TM], wb = 127u;       // exponents of the step in hand
-
-        // MFMA step kk (64 columns) of buffer buf
-        auto fragment = [&](const uint8_t *t, uint32_t r, int kk) {
-            const u32x4 lo = *reinterpret_cast<const u32x4 *>(&t[place(r, kk * 4 + half)]);
-            const u32x4 hi = *reinterpret_cast<const u32x4 *>(&t[place(r, kk * 4 + 2 + half)]);
-            i32x8 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = static_cast<int>(lo[j]);
-                v[4 + j] = static_cast<int>(hi[j]);
-            }
-            return v;
-        };
-        auto multiply = [&](auto KK, uint32_t buf) {
-            constexpr int kk = decltype(KK)::value;
-            i32x8 a[TM], b[TN];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) a[i] = fragment(sa[buf], am + i * 32 + row32, kk);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) b[j] = fragment(sb[buf], bn + j * 32 + row32, kk);
-            if constexpr (EIGHT) {
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-#pragma unroll
-                    for (int i = 0; i < TM; ++i)
-                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            a[i], b[j], acc[i][j], 0, 0, kk * 2,
-                            static_cast<int>(wa[i] >> (8 * half)), 0, static_cast<int>(wb));
-            } else {
-                const float scale_b = half_scale(wb);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    bf16x8 c[TN];
-#pragma unroll
-                    for (int j = 0; j < TN; ++j)
-                        c[j] = codes_to_bf16(static_cast<uint32_t>(b[j][2 * q]),
-                                             static_cast<uint32_t>(b[j][2 * q + 1]), scale_b);
-#pragma unroll
-                    for (int i = 0; i < TM; ++i) {
-                        const bf16x8 d = codes_to_bf16(static_cast<uint32_t>(a[i][2 * q]),
-                                                       static_cast<uint32_t>(a[i][2 * q + 1]),
-                                                       half_scale((wa[i] >> (8 * (kk * 2 + q / 2))) & 0xffu));
-#pragma unroll
-                        for (int j = 0; j < TN; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d, c[j], acc[i][j],
-                                                                                0, 0, 0);
-                    }
-                }
-            }
-        };
-
-        uint32_t eb_next = 127u;
-        if (s0 < s1) {
-            load(s0);
-            stage(0);
-            eb_next = xeb;
-            if (s0 + 1 < s1) load(s0 + 1);
-            __syncthreads();
-        }
-        for (uint32_t st = s0; st < s1; ++st) {
-            const uint32_t buf = (st - s0) & 1u;
+#pragma unroll 1
+        for (uint32_t at = s0; at < s1; ++at) {
+            trim();
+            advance();   // (up here: with a branch behind them the products are moved past it)
             wb = eb_next;
-#pragma unroll
-            for (int i = 0; i < TM; ++i) wa[i] = se[buf][am + i * 32 + row32];
-            if (st + 1 < s1) {
-                stage(buf ^ 1u);
-                eb_next = xeb;
-                if (st + 2 < s1) load(st + 2);
+            eb_next = xeb;
+            if constexpr (TN > 1) read_b(H, TN, buf, 0);
+            read_a(1, buf, 1);
+            if constexpr (TN == 1) read_b(0, 1, buf, 1);
+            stage_a(buf ^ 1u);
+            load_a(ask);
+            load_exponents(ask);
+            if constexpr (TN > 1) {
+                times(k0, 0, H);
+                interleave<kMfma * TM * H, 2 * (TN - H) + 2 * TM, PA + 1, PA + 2>();
+                read_b(0, H, buf, 1);
             }
-            multiply(std::integral_constant<int, 0>{}, buf);
-            multiply(std::integral_constant<int, 1>{}, buf);
+            stage_b(buf ^ 1u);
+            load_b(ask);
+            held = ask;
+            times(k0, H, TN);
+            interleave<kMfma * TM *(TN - H), 2 * H, PB, PB>();
+            if constexpr (TN > 1) {
+                read_b(H, TN, buf, 1);
+                times(k1, 0, H);
+                interleave<kMfma * TM * H, 2 * (TN - H), 0, 0>();
+            }
             __syncthreads();
+            read_a(0, buf ^ 1u, 0);
+            read_b(0, B1, buf ^ 1u, 0);
+            times(k1, H, TN);
+            interleave<kMfma * TM *(TN - H), 2 * B1 + 2 * TM, 0, 0>();
+            read_exponents(buf ^ 1u);
+            buf ^= 1u;
         }
-
-        if constexpr (!EIGHT) {
+        if constexpr (!CHAIN) __syncthreads();   // LDS is free
+        if constexpr (BM == 256) {
+            // The results stay in the accumulation registers until they are stored: what leaves
+            // a loop is else copied to vector registers all at once, which spills.  (The waits
+            // are a matrix instruction's, should one be in flight.)
+            asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][j][r] = acc[i][j][r] * kUnhalve;
+                for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
         }
-        // result register r of a lane: row 8 (r / 4) + 4 half + r mod 4, column lane mod 32
-        if constexpr (!SPLIT && F != 2) {
-            // each wave turns 32 rows at a time through its part of LDS into whole lines
-            constexpr uint32_t W = BN / WN, kPerRow = W / 8, kAtOnce = 64 / kPerRow;
-            constexpr uint32_t kSwap = W >= 64 ? 32 : 0;
-            static_assert(WM * WN * 32 * W * 2 <= 2 * BM * kStep, "room for 32 rows a wave");
-            uint16_t *const mine = reinterpret_cast<uint16_t *>(&sa[0][0]) + wave * (32 * W);
-            const uint32_t c = lane % kPerRow * 8, col = j0 + bn + c;
+        // Result register r of a lane: row lane mod 32, columns 8 (r / 4) + 4 half + r mod 4.
+        // Each wave turns 32 rows at a time through its part of LDS into whole lines; unit c of
+        // four columns of row r lies at c ^ 2 (r mod 16) (and the same lower bits), so that the
+        // lanes of a write fall on different banks.
+        using T = elem_t<SPLIT ? 2 : F>;
+        constexpr uint32_t W = BN / WN, kBytes = sizeof(T);
+        constexpr uint32_t kPart = W * kBytes <= 128 ? W : 128 / kBytes;   // columns at a time
+        constexpr uint32_t kUnits = kPart / 4, kLine = kPart * kBytes / 16, kAtOnce = 64 / kLine;
+        constexpr uint32_t kMask = kUnits / 2 < 16 ? kUnits / 2 - 1 : 15;
+        static_assert(32 * kPart * kBytes <= kTurn && WM * WN * kTurn <= 2 * BM * kStep, "room");
+        uint8_t *const mine = (CHAIN ? sc : &sa[0][0]) + wave * kTurn;
+        T *const out = static_cast<T *>(y) +
+                       (SPLIT ? blockIdx.y * (static_cast<uint64_t>(s.m) * s.n) : 0ull);
+        const uint64_t ld = SPLIT ? s.n : s.ldy;
+        const uint32_t turn = (row32 & kMask) * 2;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
+            for (uint32_t part = 0; part < W / kPart; ++part) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        mine[(8 * (r / 4) + 4 * half + r % 4) * W +
-                             ((j * 32 + row32) ^ (half * kSwap))] = from_f32<F>(acc[i][j][r]);
+                for (uint32_t j = part * (kPart / 32); j < (part + 1) * (kPart / 32); ++j)
+#pragma unroll
+                    for (uint32_t r = 0; r < 16; r += 4) {
+                        const uint32_t u = ((j % (kPart / 32)) * 8 + r / 2 + half) ^ turn;
+                        float v[4];
+#pragma unroll
+                        for (uint32_t t = 0; t < 4; ++t)
+                            v[t] = EIGHT ? acc[i][j][r + t] : acc[i][j][r + t] * kUnhalve;
+                        if constexpr (kBytes == 2)
+                            *reinterpret_cast<u32x2 *>(mine + row32 * (kPart * 2) + u * 8) =
+                                u32x2{pack2<F>(v[0], v[1]), pack2<F>(v[2], v[3])};
+                        else
+                            *reinterpret_cast<f32x4 *>(mine + row32 * (kPart * 4) + u * 16) =
+                                f32x4{v[0], v[1], v[2], v[3]};
+                    }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
+                const uint32_t c = lane % kLine;   // 16 B of a line
+#pragma unroll
                 for (uint32_t r0 = 0; r0 < 32; r0 += kAtOnce) {
-                    const uint32_t r = r0 + lane / kPerRow, row = i0 + am + i * 32 + r;
+                    const uint32_t r = r0 + lane / kLine, row = tile.i0 + am + i * 32 + r;
+                    const uint32_t col = tile.j0 + bn + part * kPart + c * (16 / kBytes);
+                    const uint32_t at = kBytes == 2 ? c ^ (r & kMask) : c ^ ((r & kMask) * 2);
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(
+                        mine + r * (kPart * kBytes) + at * 16);
                     if (row >= s.m || col >= n) continue;
-                    const uint16_t *v = &mine[r * W + (c ^ (((r >> 2) & 1u) * kSwap))];
-                    uint16_t *d = static_cast<uint16_t *>(y) + row * s.ldy + col;
-                    if (col + 8 <= n) {
-                        *reinterpret_cast<u32x4_any *>(d) = *reinterpret_cast<const u32x4 *>(v);
+                    T *d = out + row * ld + col;
+                    if (col + 16 / kBytes <= n) {
+                        *reinterpret_cast<u32x4_any *>(d) = v;
                     } else {
-                        for (uint32_t t = 0; t < n - col; ++t) d[t] = v[t];
+#pragma unroll
+                        for (uint32_t t = 0; t < 16 / kBytes; ++t)
+                            if (col + t < n) {
+                                if constexpr (kBytes == 2)
+                                    d[t] = static_cast<uint16_t>(v[t / 2] >> (16 * (t % 2)));
+                                else
+                                    d[t] = from_bits(v[t]);
+                            }
                     }
                 }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 __builtin_amdgcn_wave_barrier();
             }
-        } else {
-            float *const out = static_cast<float *>(y) +
-                               (SPLIT ? blockIdx.y * (static_cast<uint64_t>(s.m) * s.n) : 0ull);
-            const uint64_t ld = SPLIT ? s.n : s.ldy;
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const uint32_t row = i0 + am + i * 32 + 8 * (r / 4) + 4 * half + r % 4;
-                    if (row >= s.m) continue;
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) {
-                        const uint32_t col = j0 + bn + j * 32 + row32;
-                        if (col < n) out[row * ld + col] = acc[i][j][r];
-                    }
-                }
-        }
-        __syncthreads();   // the next tile writes LDS
+        if constexpr (!CHAIN) __syncthreads();   // the next tile writes LDS
     }
 }
 
@@ -454,18 +633,33 @@ bool tiled(uint64_t k) { return k >= 16 && k < kMaxLength; }
 template <int F, bool EIGHT, bool SPLIT>
 hipError_t tiles_of(const ProductArgs &a, const ProductShape &s, const Plan &p,
                     hipStream_t stream) {
-    const dim3 grid(capped(s.work), p.splits);
+    // workgroups that fill the chip once, each with its tiles in turn
+    const uint64_t fill = kFill * (p.tile == 256 ? 1 : p.tile == 128 ? 2 : 4);
+    const dim3 grid(capped(s.work < fill ? s.work : fill), p.splits);
     void *out = SPLIT ? a.workspace : a.y;
-#define ZS_TILE(B, WM, WN)                                                                   \
-    product_tile_kernel<F, EIGHT, SPLIT, B, B, WM, WN>                                       \
+    const bool a32 = a.a_block == ZERO_ACT_BLOCK, ragged = a.k % kStep != 0;
+#define ZS_FORM(A32, RAGGED, B, WM, WN)                                                      \
+    product_tile_kernel<F, EIGHT, SPLIT, A32, RAGGED, B, B, WM, WN>                          \
         <<<grid, 64 * WM * WN, 0, stream>>>(out, a.qa, a.ea, a.qb, a.eb, s)
+#define ZS_TILE(B, WM, WN)                                                                   \
+    do {                                                                                     \
+        if (a32 && ragged)                                                                   \
+            ZS_FORM(true, true, B, WM, WN);                                                  \
+        else if (a32)                                                                        \
+            ZS_FORM(true, false, B, WM, WN);                                                 \
+        else if (ragged)                                                                     \
+            ZS_FORM(false, true, B, WM, WN);                                                 \
+        else                                                                                 \
+            ZS_FORM(false, false, B, WM, WN);                                                \
+    } while (0)
     if (p.tile == 256)
-        ZS_TILE(256, 4, 2);
+        ZS_TILE(256, 2, 2);
     else if (p.tile == 128)
         ZS_TILE(128, 2, 2);
     else
         ZS_TILE(64, 2, 2);
 #undef ZS_TILE
+#undef ZS_FORM
     return hipGetLastError();
 }
 
