@@ -83,9 +83,9 @@ __device__ __forceinline__ void deal() {
         deal<I + 1, M, R, W, G>();
     }
 }
-template <int M, int R, int W, int G>
+template <bool EIGHT, int M, int R, int W, int G>
 __device__ __forceinline__ void interleave() {
-    deal<0, M, R, W, G>();
+    if constexpr (EIGHT) deal<0, M, R, W, G>();
     __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -97,29 +97,9 @@ struct ProductShape {
     uint32_t blocks_a, blocks_b;   // exponent bytes a row of a, and of b's blocks
     uint32_t shift_a;              // log2 of a's block
     uint32_t per_split;            // steps a split
-    uint32_t tiles_m, tiles_n;
-    uint32_t group_n;              // tiles a group has along n, 0: no groups
-    uint64_t work;                 // work items: tiles, or places in groups
+    uint32_t tiles_n;
+    uint64_t work;                 // tiles, along n first (grouped by XCD they took the same time)
 };
-
-// Tile of work item w: tiles in groups of 32 (`group_n` along n), groups dealt to the eight
-// XCDs in turn (workgroups go round them by number), so that the 32 compute units of an XCD
-// share operands in its L2.  false: no such tile.
-__device__ __forceinline__ bool tile_of(const ProductShape &s, uint64_t w, uint32_t *i,
-                                        uint32_t *j) {
-    if (s.group_n == 0) {
-        *i = static_cast<uint32_t>(w / s.tiles_n);
-        *j = static_cast<uint32_t>(w - static_cast<uint64_t>(*i) * s.tiles_n);
-        return true;
-    }
-    const uint32_t group_m = 32 / s.group_n, across = (s.tiles_n + s.group_n - 1) / s.group_n;
-    const uint64_t at = w >> 3, group = (at >> 5) * 8 + (w & 7);
-    const uint32_t in = static_cast<uint32_t>(at & 31);
-    const uint64_t gi = group / across;
-    *i = static_cast<uint32_t>(gi) * group_m + in % group_m;
-    *j = static_cast<uint32_t>(group - gi * across) * s.group_n + in / group_m;
-    return gi * group_m < s.tiles_m && *i < s.tiles_m && *j < s.tiles_n;
-}
 
 // BM x BN tiles of y (or, SPLIT, of a split's FP32 plane); WM x WN waves.  EIGHT: the 8-bit
 // instruction.  A32: a's blocks are of 32 columns.  RAGGED: the last step is short.  Rows past the matrix are read as its last
@@ -170,19 +150,12 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
         get[c] = row32 * kStep + (((2u * c + half) ^ ((row32 >> 1) & 7u)) << 4);
 
     struct Tile {
-        uint32_t i0, j0;
+        uint32_t i0, j0;   // its first row and column
     };
-    // the first place from `at` on that has a tile
-    auto seek = [&](uint64_t at, Tile *t) {
-        for (; at < s.work; at += gridDim.x) {
-            uint32_t ti, tj;
-            const bool found = tile_of(s, at, &ti, &tj);
-            if (!uniform(found)) continue;
-            t->i0 = uniform(ti) * BM;
-            t->j0 = uniform(tj) * BN;
-            break;
-        }
-        return at;
+    auto tile_at = [&](uint64_t w) {
+        const uint64_t i = w / s.tiles_n;
+        return Tile{uniform(static_cast<uint32_t>(i)) * BM,
+                    uniform(static_cast<uint32_t>(w - i * s.tiles_n)) * BN};
     };
 
     // what is requested: step `ask` of tile `from`
@@ -303,15 +276,11 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
     auto advance = [&]() {
         if (ask + 1 < s1) {
             ++ask;
-        } else if constexpr (CHAIN) {
-            Tile t{0, 0};
-            const uint64_t at = seek(asked + gridDim.x, &t);
-            if (at < s.work) {
-                asked = at;
-                from = t;
-                ask = s0;
-                aim();
-            }
+        } else if (CHAIN && asked + gridDim.x < s.work) {
+            asked += gridDim.x;
+            from = tile_at(asked);
+            ask = s0;
+            aim();
         }
     };
 
@@ -388,7 +357,6 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
     // of b's first half and of a for the next MFMA step, those of b's second half as the first
     // half is multiplied.  The barrier stands where every wave has this buffer's last fragments
     // in registers and its share of the next buffer written.
-    constexpr int kMfma = EIGHT ? 1 : 4;   // instructions a product of 64 columns
     constexpr int B1 = TN > 1 ? H : 1;
     uint32_t eb_next = 127u, buf = 0;
     auto begin = [&]() {
@@ -406,12 +374,9 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
         read_b(0, B1, 0, 0);
     };
 
-    Tile tile{0, 0};
-    uint64_t work = seek(blockIdx.x, &tile);
-    bool begun = false;
-    for (; work < s.work; work = seek(work + gridDim.x, &tile)) {
-        if (!CHAIN || !begun) {
-            begun = true;
+    for (uint64_t work = blockIdx.x; work < s.work; work += gridDim.x) {
+        const Tile tile = tile_at(work);
+        if (!CHAIN || work == blockIdx.x) {
             asked = work;
             from = tile;
             ask = s0;
@@ -438,24 +403,24 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
             load_exponents(ask);
             if constexpr (TN > 1) {
                 times(k0, 0, H);
-                interleave<kMfma * TM * H, 2 * (TN - H) + 2 * TM, PA + 1, PA + 2>();
+                interleave<EIGHT, TM * H, 2 * (TN - H) + 2 * TM, PA + 1, PA + 2>();
                 read_b(0, H, buf, 1);
             }
             stage_b(buf ^ 1u);
             load_b(ask);
             held = ask;
             times(k0, H, TN);
-            interleave<kMfma * TM *(TN - H), 2 * H, PB, PB>();
+            interleave<EIGHT, TM * (TN - H), 2 * H, PB, PB>();
             if constexpr (TN > 1) {
                 read_b(H, TN, buf, 1);
                 times(k1, 0, H);
-                interleave<kMfma * TM * H, 2 * (TN - H), 0, 0>();
+                interleave<EIGHT, TM * H, 2 * (TN - H), 0, 0>();
             }
             __syncthreads();
             read_a(0, buf ^ 1u, 0);
             read_b(0, B1, buf ^ 1u, 0);
             times(k1, H, TN);
-            interleave<kMfma * TM *(TN - H), 2 * B1 + 2 * TM, 0, 0>();
+            interleave<EIGHT, TM * (TN - H), 2 * B1 + 2 * TM, 0, 0>();
             read_exponents(buf ^ 1u);
             buf ^= 1u;
         }
@@ -518,7 +483,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
                     if (row >= s.m || col >= n) continue;
                     T *d = out + row * ld + col;
                     if (col + 16 / kBytes <= n) {
-                        *reinterpret_cast<u32x4_any *>(d) = v;
+                        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any *>(d));
                     } else {
 #pragma unroll
                         for (uint32_t t = 0; t < 16 / kBytes; ++t)
@@ -601,24 +566,36 @@ struct Plan {
 constexpr uint64_t kFill = 256;              // compute units of the chip
 constexpr uint64_t kMaxLength = 1ull << 24;  // a tile's rows stay below 2^32 bytes
 
+// Measured on MI355X, in ns: a step of 128 columns of a tile that has a compute unit to itself,
+// its share of one where several run side by side (`resident` at most), and a tile's start and
+// end.  The large tile uses each operand most but fills and drains slowly; a small one starts
+// quickly and is bound by latency.
 struct TileCost {
-    uint32_t tile, step, ends;   // ns: a step of 128 columns, a tile's start and end
+    uint32_t tile, resident, alone, shared, ends;
 };
-constexpr TileCost kTiles[3] = {{256, 1100, 8000}, {128, 500, 4000}, {64, 300, 2500}};
+constexpr TileCost kTiles[3] = {
+    {256, 1, 1500, 1500, 9000}, {128, 2, 620, 500, 4000}, {64, 4, 400, 240, 3000}};
 
+// The tile and splits of least estimated time; splits cost the join's launch and its planes,
+// written and read.  Over nine shapes of 1 to 2048 rows, 768 to 50257 columns and 768 to 8192
+// summed ones the choice was within 10% of the best of every tile with 1 to 16 splits: 1024 x
+// 1024 x 8192, for example, takes 24 us in 128 x 128 tiles and 4 splits, 46 in one, 34 in 64 x
+// 64 tiles and 38 in 256 x 256 and 8 splits; 1 x 8192 x 8192 15.6 us in 64 x 64 and 4, 30 in one.
 Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
     const uint64_t steps = (k + kStep - 1) / kStep;
-    const uint64_t plane_ns = m * n / 1000;
     Plan best{0, 1, 0};
     uint64_t best_ns = ~0ull;
     for (const TileCost &c : kTiles) {
         const uint64_t tiles = ((m + c.tile - 1) / c.tile) * ((n + c.tile - 1) / c.tile);
-        for (uint64_t s = 1; s <= 64 && s <= steps && (s == 1 || tiles * s <= 2 * kFill); ++s) {
+        for (uint64_t s = 1; s <= 64 && s <= steps && (s == 1 || tiles * s <= 4 * kFill); ++s) {
             const uint64_t per = (steps + s - 1) / s, used = (steps + per - 1) / per;
             if (used != s) continue;
-            const uint64_t rounds = (tiles * s + kFill - 1) / kFill;
-            uint64_t ns = rounds * (per * c.step + c.ends);
-            if (s > 1) ns += 5000 + s * (plane_ns + 150);
+            const uint64_t each = (tiles * s + kFill - 1) / kFill;   // of a compute unit
+            const uint64_t beside = each < c.resident ? each : c.resident;
+            const uint64_t step =
+                beside * c.shared > c.alone ? beside * c.shared : c.alone;
+            uint64_t ns = (each + c.resident - 1) / c.resident * (per * step + c.ends);
+            if (s > 1) ns += 2500 + s * (m * n / 625);   // 8 B a result at 5 TB/s
             if (ns < best_ns) {
                 best_ns = ns;
                 best = Plan{c.tile, static_cast<uint32_t>(s), static_cast<uint32_t>(per)};
@@ -676,24 +653,12 @@ hipError_t product_as(const ProductArgs &a, hipStream_t stream) {
                    static_cast<uint32_t>((a.k + ZERO_BLOCK - 1) / ZERO_BLOCK),
                    a.a_block == ZERO_BLOCK ? 7u : 5u,
                    p.per_split,
-                   static_cast<uint32_t>(tiles_m),
                    static_cast<uint32_t>(tiles_n),
-                   0,
                    tiles_m * tiles_n};
     if (!tiled(a.k)) {
         product_plain_kernel<F><<<capped((a.m * a.n + kThreads - 1) / kThreads), kThreads, 0,
                                   stream>>>(y, a.qa, a.ea, a.qb, a.eb, s);
         return hipGetLastError();
-    }
-    // groups where they leave few places empty (empty ones cost the XCDs' balance)
-    for (uint32_t gn = 8; gn > 0 && s.group_n == 0 && s.work >= kFill; gn /= 2) {
-        const uint64_t gm = 32 / gn;
-        const uint64_t groups = ((tiles_m + gm - 1) / gm) * ((tiles_n + gn - 1) / gn);
-        const uint64_t places = (groups + 7) / 8 * 8 * 32;
-        if (places * 8 <= s.work * 9) {
-            s.group_n = gn;
-            s.work = places;
-        }
     }
     if (p.splits == 1) return tiles_of<F, F != 2, false>(a, s, p, stream);
     const hipError_t e = tiles_of<F, F != 2, true>(a, s, p, stream);
