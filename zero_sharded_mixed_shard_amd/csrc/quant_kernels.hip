@@ -16,7 +16,7 @@
 // on all of its 32 banks.
 //
 // These kernels are streams over HBM.
-#include "block_launch.h"
+#include "block_device.h"
 #include "code_device.h"
 
 #pragma clang fp contract(off)
@@ -99,6 +99,22 @@ __global__ __launch_bounds__(kThreads) void quant_row_kernel(
     }
 }
 
+// Eight values of format F as raw bits.
+template <int F>
+__device__ __forceinline__ Raw8<F> narrow8(const float v[8]) {
+    Raw8<F> r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (F == 2) {
+            r.v[0][j] = bits(v[j]);
+            r.v[1][j] = bits(v[4 + j]);
+        } else {
+            r.v[0][j] = pack2<F>(v[2 * j], v[2 * j + 1]);
+        }
+    }
+    return r;
+}
+
 // Four rows of four bytes as four columns.
 __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
                                            uint32_t out[4]) {
@@ -113,8 +129,10 @@ __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, u
 }
 
 // One 128 x 128 block a workgroup; lane (tr, tc) of 16 x 16 holds rows 8 tr .. 8 tr + 7 of
-// columns 8 tc .. 8 tc + 7.
-template <int F, bool TRANSPOSED>
+// columns 8 tc .. 8 tc + 7, as they lie in memory (widened twice, for the maximum and for the
+// codes: held as FP32 they take the registers of every second workgroup).  NARROW: rows of
+// less than eight columns.
+template <int F, bool TRANSPOSED, bool NARROW>
 __global__ __launch_bounds__(kThreads) void quant_square_kernel(
     uint8_t *__restrict__ q, uint8_t *__restrict__ e, uint8_t *__restrict__ qt,
     uint8_t *__restrict__ et, const elem_t<F> *__restrict__ x, uint64_t ldx, uint64_t rows,
@@ -126,20 +144,35 @@ __global__ __launch_bounds__(kThreads) void quant_square_kernel(
     for (uint64_t blk = blockIdx.x; blk < n_blocks; blk += gridDim.x, parity ^= 1u) {
         const uint64_t br = div_by(blk, nb), bc = blk - br * nb.d;
         const uint64_t r0 = br * ZERO_BLOCK + tr * 8, c0 = bc * ZERO_BLOCK + tc * 8;
-        float v[8][8];
+        const uint32_t n = group_size(c0, cols);
+        Raw8<F> raw[8];
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-            if (r0 + p < rows) {
-                load_group<F>(x + (r0 + p) * ldx, c0, cols, v[p]);
+            const elem_t<F> *row = x + (r0 + p < rows ? r0 + p : rows - 1) * ldx;
+            if constexpr (NARROW) {
+                float v[8];
+                load_some<F>(row + c0, n, v);
+                raw[p] = narrow8<F>(v);
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[p][j] = 0.0f;
+                raw[p] = raw_group<F>(row, static_cast<uint32_t>(c0),
+                                      static_cast<uint32_t>(cols));
             }
+        }
+        if (!NARROW && n - 1u < 7u) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p) move_down<F>(raw[p], n);
+        }
+        if (n == 0 || r0 + 8 > rows) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                if (n == 0 || r0 + p >= rows) raw[p] = Raw8<F>{};
         }
         uint32_t m = 0;
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-            const uint32_t a = magnitude8(v[p]);
+            float v[8];
+            widen8<F>(raw[p], v);
+            const uint32_t a = magnitude8(v);
             m = a > m ? a : m;
         }
         const bool rare = __any(m > bits(kTop<F>));
@@ -147,7 +180,9 @@ __global__ __launch_bounds__(kThreads) void quant_square_kernel(
             m = 0;
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
-                const uint32_t a = finite_magnitude8(v[p]);
+                float v[8];
+                widen8<F>(raw[p], v);
+                const uint32_t a = finite_magnitude8(v);
                 m = a > m ? a : m;
             }
         }
@@ -168,9 +203,12 @@ __global__ __launch_bounds__(kThreads) void quant_square_kernel(
         const uint32_t eb = block_exponent(m);
         u32x2 c[8];
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-            c[p] = rare ? encode8<F, true>(v[p], eb) : encode8<F, false>(v[p], eb);
-        const uint32_t n = group_size(c0, cols);
+        for (int p = 0; p < 8; ++p) {
+            float v[8];
+            asm volatile("" : "+v"(raw[p].v[0]));   // widened anew, not kept from above
+            widen8<F>(raw[p], v);
+            c[p] = rare ? encode8<F, true>(v, eb) : encode8<F, false>(v, eb);
+        }
 #pragma unroll
         for (int p = 0; p < 8; ++p)
             if (r0 + p < rows) store_codes(q + (r0 + p) * cols + c0, n, c[p]);
@@ -270,12 +308,18 @@ hipError_t quant_as(uint8_t *q, uint8_t *e, uint8_t *qt, uint8_t *et, const void
                                                                             div, groups);
     } else {
         const uint64_t blocks = nb * ((rows + ZERO_BLOCK - 1) / ZERO_BLOCK);
-        if (qt != nullptr)
-            quant_square_kernel<F, true><<<grid_of(blocks), kThreads, 0, stream>>>(
-                q, e, qt, et, xt, ldx, rows, cols, div, blocks);
+#define ZS_SQUARE(TRANSPOSED, NARROW)                                                        \
+    quant_square_kernel<F, TRANSPOSED, NARROW><<<grid_of(blocks), kThreads, 0, stream>>>(    \
+        q, e, qt, et, xt, ldx, rows, cols, div, blocks)
+        if (cols < 8 && qt != nullptr)
+            ZS_SQUARE(true, true);
+        else if (cols < 8)
+            ZS_SQUARE(false, true);
+        else if (qt != nullptr)
+            ZS_SQUARE(true, false);
         else
-            quant_square_kernel<F, false><<<grid_of(blocks), kThreads, 0, stream>>>(
-                q, e, qt, et, xt, ldx, rows, cols, div, blocks);
+            ZS_SQUARE(false, false);
+#undef ZS_SQUARE
     }
     return hipGetLastError();
 }

@@ -414,41 +414,6 @@ __global__ __launch_bounds__(kWideThreads) void wide_backward_kernel(
 
 constexpr int kRowWaves = 16;   // most waves of a workgroup
 
-// Eight columns of a row from col on, read without a branch: where the row ends inside or
-// before them, its last eight (the row has eight at least).
-template <int F>
-__device__ __forceinline__ Raw8<F> raw_group(const elem_t<F> *row, uint32_t col, uint32_t cols) {
-    return load8<F>(row + (col + 8 <= cols ? col : cols - 8));
-}
-
-// What was read as the row's last eight, moved down to the n (1 to 7) that are the lane's,
-// zeros above.
-template <int F>
-__device__ __forceinline__ void move_down(Raw8<F> &r, uint32_t n) {
-    constexpr int kWords = F == 2 ? 8 : 4;
-    uint32_t w[kWords];
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) w[j] = r.v[j / 4][j % 4];
-    const uint32_t by = 8 - n;   // elements
-    if constexpr (F != 2) {
-        if (by & 1u) {
-#pragma unroll
-            for (int j = 0; j < kWords; ++j)
-                w[j] = w[j] >> 16 | (j + 1 < kWords ? w[j + 1] << 16 : 0u);
-        }
-    }
-#pragma unroll
-    for (int k = F == 2 ? 1 : 2; k < 8; k *= 2) {
-        const int words = F == 2 ? k : k / 2;
-        if (by & static_cast<uint32_t>(k)) {
-#pragma unroll
-            for (int j = 0; j < kWords; ++j) w[j] = j + words < kWords ? w[j + words] : 0u;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) r.v[j / 4][j % 4] = w[j];
-}
-
 // The n (0 to 8) columns of a group that are the lane's, zeros past them; ragged: the row's
 // length is no multiple of eight.
 template <int F>
