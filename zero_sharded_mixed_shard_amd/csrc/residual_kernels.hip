@@ -663,8 +663,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void row_forward_kernel(
 template <int F, int R, int V, int WAVES, bool BIAS>
 __global__ __launch_bounds__(64 * WAVES) void row_backward_kernel(
     Step s, uint32_t waves, Back<F, R> p, float *__restrict__ part, uint32_t parts) {
-    constexpr bool kHeld = true;
+    // Rows of more than 8192 columns: sum dh u^ and sum G f^ of a lane's columns are kept in LDS
+    // and factors read again for each row, or the registers would not suffice (16 waves of 128).
+    constexpr bool kLong = V == 2 && WAVES == 16, kHeld = !kLong;
     __shared__ float slots[2][2][kRowWaves];
+    __shared__ __align__(16) float kept[kLong ? 2 : 1][kLong ? kRowWaves * 1024 : 4];
     extern __shared__ float joined[];   // [rows at once][cols], W == 1 only
     RowTotal total(slots, waves);
     const MaskKey key(s.mask);
@@ -681,7 +684,35 @@ __global__ __launch_bounds__(64 * WAVES) void row_backward_kernel(
     w2.hold(mine);
     for (uint32_t q = blockIdx.x; q < parts; q += gridDim.x) {
         uint64_t row = static_cast<uint64_t>(q) * at_once + (waves == 1 ? total.wave : 0u);
-        float sums[BIAS ? 4 : 2][V][8] = {};
+        // sum dh u^, sum dh, sum G f^, sum G
+        float sums[4][V][8] = {};
+        if constexpr (kLong) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4)
+                        *reinterpret_cast<f32x4 *>(&kept[k][mine.col(v) + j]) =
+                            f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        // sums[k] + x y of group v (k: 0 or 2)
+        auto add = [&](int k, int v, const float *x, const float *y) {
+            if constexpr (kLong) {
+                float *d = &kept[k / 2][mine.col(v)];
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    f32x4 t = *reinterpret_cast<f32x4 *>(d + j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t[i] = __builtin_fmaf(x[j + i], y[j + i], t[i]);
+                    *reinterpret_cast<f32x4 *>(d + j) = t;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sums[k][v][j] = __builtin_fmaf(x[j], y[j], sums[k][v][j]);
+            }
+        };
         Raw8<F> raw_dh[V], raw_f[V];
         Raw8<R> raw_u[V], raw_du[V];
         auto fetch_pre = [&](uint64_t t) {
@@ -732,9 +763,9 @@ __global__ __launch_bounds__(64 * WAVES) void row_backward_kernel(
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         z[v][j] = z[v][j] * rho2;
-                        sums[0][v][j] = __builtin_fmaf(g[v][j], z[v][j], sums[0][v][j]);
                         if constexpr (BIAS) sums[1][v][j] = sums[1][v][j] + g[v][j];
                     }
+                    add(0, v, g[v], z[v]);
                     if (w2.there()) {
                         const float *w = w2.at(mine, v);
 #pragma unroll
@@ -802,11 +833,10 @@ __global__ __launch_bounds__(64 * WAVES) void row_backward_kernel(
 #pragma unroll
                     for (int j = 0; j < 8; ++j) fh[v][j] = fh[v][j] * rho1;
                 }
+                add(2, v, G[v], fh[v]);
+                if constexpr (BIAS) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    constexpr int kA = BIAS ? 2 : 1;
-                    sums[kA][v][j] = __builtin_fmaf(G[v][j], fh[v][j], sums[kA][v][j]);
-                    if constexpr (BIAS) sums[3][v][j] = sums[3][v][j] + G[v][j];
+                    for (int j = 0; j < 8; ++j) sums[3][v][j] = sums[3][v][j] + G[v][j];
                 }
                 if (w1.there()) {
                     const float *w = w1.at(mine, v);
@@ -849,12 +879,14 @@ __global__ __launch_bounds__(64 * WAVES) void row_backward_kernel(
         // sum k of this part: of one wave's rows (W > 1: of the workgroup's), or of its waves'
         // in their order
 #pragma unroll
-        for (int k = 0; k < (BIAS ? 4 : 2); ++k) {
-            float *d = part + (static_cast<uint64_t>(q) * 4 + (BIAS ? k : 2 * k)) * s.cols;
+        for (int k = 0; k < 4; k += BIAS ? 1 : 2) {
+            float *d = part + (static_cast<uint64_t>(q) * 4 + k) * s.cols;
             if (at_once == 1) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    if (mine.n(v) != 0) store_row<2>(d, mine.col(v), mine.n(v), sums[k][v]);
+                    if (mine.n(v) != 0)
+                        store_row<2>(d, mine.col(v), mine.n(v),
+                                     kLong && k % 2 == 0 ? &kept[k / 2][mine.col(v)] : sums[k][v]);
                 continue;
             }
             __syncthreads();
@@ -964,22 +996,27 @@ uint32_t waves_of(uint64_t cols, int groups) {
     return static_cast<uint32_t>((cols + span - 1) / span);
 }
 
-// What a lane holds wants 256 registers rather than 128.
+// How much a lane of the backward pass holds: 16-bit data with two sums, with four or beside an
+// FP32 stream, or FP32 data and four sums beside an FP32 stream.
+enum class Load { kLight, kMiddle, kHeavy };
 template <int F, int R>
-constexpr bool roomy(bool bias_sums) {
-    return F == 2 || (R == 2 && bias_sums);
+constexpr Load load_of(bool bias_sums) {
+    if (F == 2 || (R == 2 && bias_sums)) return Load::kHeavy;
+    return R == 2 || bias_sums ? Load::kMiddle : Load::kLight;
 }
 
 // The backward pass: rows of one wave up to 1024 columns, so that a workgroup joins eight
 // rows' sums before it writes them; up to 8192 columns rows of several waves, one group a lane
-// (16 waves of 128 registers), or two (`roomy`, 8 of 256) where more is held: the four sums
-// beside FP32 data (16384 x 8192: 770 us against 844; 16-bit data with two sums: 378 against
-// 348).  As many parts as fill the chip once.
-RowPlan backward_plan(uint64_t rows, uint64_t cols, bool roomy) {
+// (16 waves of 128 registers), or two for what is heavy (8 of 256: 16384 x 8192 FP32, four
+// sums, 770 us against 844; 16-bit data with two sums: 378 against 348); up to 16384 columns
+// two groups of 16 waves for what is light (8192 x 12288 BF16: 355 us, walked over in memory
+// 607; with an FP32 stream 818 and 704).  As many parts as fill the chip once.
+RowPlan backward_plan(uint64_t rows, uint64_t cols, Load load) {
     const uint64_t per = (rows + kUnits - 1) / kUnits;
     RowPlan p{0, 1, 1, static_cast<uint32_t>((rows + per - 1) / per)};
-    if (cols > 8192 || cols < 8) return p;
-    p.groups = cols > 512 && (cols <= 1024 || roomy) ? 2 : 1;
+    if (cols > (load == Load::kLight ? 16384u : 8192u) || cols < 8) return p;
+    p.groups =
+        cols > 8192 || (cols > 512 && (cols <= 1024 || load == Load::kHeavy)) ? 2 : 1;
     p.waves = waves_of(cols, p.groups);
     if (p.waves == 1) p.at_once = static_cast<uint32_t>(rows < 8 ? rows : 8);
     const uint64_t resident = (p.groups == 1 ? 16 : 8) / (p.waves * p.at_once);
@@ -1025,13 +1062,17 @@ hipError_t rows_backward(const Step &s, const RowPlan &plan, const Back<F, R> &p
                          hipStream_t stream) {
     const uint32_t threads = 64 * plan.waves * plan.at_once, grid = capped(plan.parts);
     const size_t lds = plan.at_once > 1 ? sizeof(float) * plan.at_once * s.cols : 0;
-    constexpr bool kRoomy = roomy<F, R>(BIAS);
+    constexpr Load kLoad = load_of<F, R>(BIAS);
+#define ZS_ROWS(V, WAVES)                                                                    \
+    row_backward_kernel<F, R, V, WAVES, BIAS><<<grid, threads, lds, stream>>>(               \
+        s, plan.waves, p, part, plan.parts)
     if (plan.groups == 1)
-        row_backward_kernel<F, R, 1, kRoomy ? 8 : 16, BIAS><<<grid, threads, lds, stream>>>(
-            s, plan.waves, p, part, plan.parts);
+        ZS_ROWS(1, kLoad == Load::kHeavy ? 8 : 16);
+    else if (kLoad != Load::kLight || plan.waves <= 8)
+        ZS_ROWS(2, 8);
     else
-        row_backward_kernel<F, R, 2, 8, BIAS><<<grid, threads, lds, stream>>>(
-            s, plan.waves, p, part, plan.parts);
+        ZS_ROWS(2, kLoad == Load::kLight ? 16 : 8);
+#undef ZS_ROWS
     return hipGetLastError();
 }
 
@@ -1045,7 +1086,7 @@ hipError_t backward_as(const ResidualArgs &a, hipStream_t stream) {
     float *part = static_cast<float *>(a.workspace);
     bool bias_sums = a.db1 != nullptr || a.db2 != nullptr ||
                      (a.dgate != nullptr && a.b1 != nullptr);
-    const RowPlan plan = backward_plan(a.rows, a.cols, roomy<F, R>(bias_sums));
+    const RowPlan plan = backward_plan(a.rows, a.cols, load_of<F, R>(bias_sums));
     hipError_t e;
     if (plan.groups == 0) {
         bias_sums = true;
@@ -1078,8 +1119,13 @@ hipError_t backward_as(const ResidualArgs &a, hipStream_t stream) {
 }  // namespace
 
 uint64_t residual_workspace(uint64_t rows, uint64_t cols) {
-    const RowPlan p = backward_plan(rows, cols, false), q = backward_plan(rows, cols, true);
-    return ((p.parts > q.parts ? p.parts : q.parts) * cols + (p.groups == 0 ? rows : 0)) * 16;
+    uint64_t bytes = 0;
+    for (const Load load : {Load::kLight, Load::kMiddle, Load::kHeavy}) {
+        const RowPlan p = backward_plan(rows, cols, load);
+        const uint64_t n = (p.parts * cols + (p.groups == 0 ? rows : 0)) * 16;
+        bytes = n > bytes ? n : bytes;
+    }
+    return bytes;
 }
 
 hipError_t launch_residual_forward(const ResidualArgs &a, hipStream_t stream) {
