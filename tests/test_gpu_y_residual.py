@@ -314,3 +314,13 @@ def test_refusals():
     for bad in (dict(workspace=None), dict(d_gate=g.bfloat16(), first=False), dict(eps=0.0)):
         with pytest.raises(zs.ZeroError):
             zs.zero_residual_norm_backward(**dict(a, **bad))
+
+
+@pytest.mark.parametrize("cols", [60, 3000, 20000])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_a_large_epsilon_beside_large_values(cols, kind):
+    # where rows are summed scaled, epsilon is still part of the deviation
+    for eps, size in ((1e36, 1e18), (1e38, 1e19), (1e30, 1e18)):
+        c = Case(5, cols, "bf16", "f32", kind, kind, bias=False, p=0.0, size=size, gate=False,
+                 eps=eps, scale=1.0)
+        c.check_forward()

@@ -62,9 +62,9 @@ __device__ __forceinline__ void row_stats(int kind, float cols, float eps, Total
     constexpr float k = 0x1p-80f;
     m = kind == ZERO_NORM_LAYER ? total([](float x) { return x * k; }) / cols : 0.0f;
     ss = total([m](float x) { return (x * k - m) * (x * k - m); });
-    const float v = ss / cols;
+    const float v = ss / cols + eps * k * k;
     *mean = m * 0x1p80f;
-    *rho = 1.0f / sqrtf(v < 0x1p-120f ? 0x1p-120f : v) * k;   // eps k^2 is far below v; a NaN stays
+    *rho = 1.0f / sqrtf(v < 0x1p-120f ? 0x1p-120f : v) * k;   // equal values: no quotient by 0
 }
 
 // Eight values of a parameter from column col on: `other` where there is none.
@@ -233,9 +233,8 @@ struct RowMeans {
 
 // u^ and dh of eight columns.
 template <int F, int R>
-__device__ __forceinline__ void pre8(const Step &s, const Back<F, R> &p, uint64_t row,
-                                     uint32_t col, uint32_t n, const RowMeans &m, float dh[8],
-                                     float uhat[8]) {
+__device__ __forceinline__ void pre8(const Back<F, R> &p, uint64_t row, uint32_t col, uint32_t n,
+                                     const RowMeans &m, float dh[8], float uhat[8]) {
     if (p.dh == nullptr) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) dh[j] = uhat[j] = 0.0f;
@@ -245,7 +244,6 @@ __device__ __forceinline__ void pre8(const Step &s, const Back<F, R> &p, uint64_
     load_row<R>(p.u + row * p.ldu, col, n, uhat);
 #pragma unroll
     for (int j = 0; j < 8; ++j) uhat[j] = (uhat[j] - m.mean2) * m.rho2;
-    (void)s;
 }
 
 // G' of eight columns from dh and u^; w2: the pre norm's weight there.
@@ -299,7 +297,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_means_kernel(Step s, Back<F
                 const uint32_t col = static_cast<uint32_t>(c);
                 const uint32_t n = s.cols - col < 8 ? s.cols - col : 8u;
                 float dh[8], uhat[8], w2[8];
-                pre8(s, p, row, col, n, m, dh, uhat);
+                pre8(p, row, col, n, m, dh, uhat);
                 load_param<F>(s.w2, col, n, 1.0f, w2);
 #pragma unroll
                 for (uint32_t j = 0; j < 8; ++j) {
@@ -317,7 +315,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_means_kernel(Step s, Back<F
                 const uint32_t col = static_cast<uint32_t>(c);
                 const uint32_t n = s.cols - col < 8 ? s.cols - col : 8u;
                 float dh[8], uhat[8], G[8], fhat[8], w[8];
-                pre8(s, p, row, col, n, m, dh, uhat);
+                pre8(p, row, col, n, m, dh, uhat);
                 load_param<F>(s.w2, col, n, 1.0f, w);
                 stream8(p, row, col, n, m, dh, uhat, w, G);
                 post8(s, key, p, row, col, n, m, G, fhat);
@@ -367,7 +365,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_backward_kernel(
             const float *st = p.stats + row * 4, *mn = means + row * 4;
             const RowMeans m{st[0], st[1], st[2], st[3], mn[0], mn[1], mn[2], mn[3]};
             float dh[8], uhat[8], G[8], fhat[8], out[8];
-            pre8(s, p, row, col, n, m, dh, uhat);
+            pre8(p, row, col, n, m, dh, uhat);
             stream8(p, row, col, n, m, dh, uhat, w2, G);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
