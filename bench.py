@@ -555,6 +555,76 @@ def measure_gradient_operators(dev, reps: int = 5) -> dict:
     return out
 
 
+def measure_block_operators(dev, reps: int = 5) -> dict:
+    """The operators around a block's linear layers (HIP events), on a 16384-token micro-batch
+    of a wide layer: algorithmic GB/s, and TFLOP/s of the product."""
+    import torch
+
+    import synth
+    import zero_sharded_mixed_shard_amd as zs
+
+    out = {}
+    stream = torch.cuda.current_stream(dev)
+    bf16 = torch.bfloat16
+
+    def record(name, nbytes, fn, flops=None):
+        fn()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record(stream)
+        for _ in range(reps):
+            fn()
+        e1.record(stream)
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / reps
+        gbps = nbytes / (ms * 1e-3) / 1e9
+        out[name] = {"ms": ms, "GBps": gbps, "frac": gbps / PEAK_HBM_GBPS}
+        if flops is not None:
+            out[name]["TFLOPs"] = flops / (ms * 1e-3) / 1e12
+
+    def normal(rows, cols, std, seed, dtype=bf16):
+        flat = torch.empty(rows * cols, dtype=dtype, device=dev)
+        return synth.fill_normal_(flat, std, seed).view(rows, cols)
+
+    def u8(*shape):
+        return torch.empty(shape, dtype=torch.uint8, device=dev)
+
+    tokens, width, hidden = 16384, 4096, 8192
+    x, w = normal(tokens, width, 1.0, 41), normal(hidden, width, 0.02, 42)
+    qx, ex = u8(tokens, width), u8(tokens, width // zs.BLOCK)
+    qw, ew = u8(hidden, width), u8(hidden // zs.BLOCK, width // zs.BLOCK)
+    qt, et = u8(width, hidden), u8(width // zs.BLOCK, hidden // zs.BLOCK)
+    record("block_quant", 3 * x.numel() + ex.numel(), lambda: zs.zero_block_quant(qx, ex, x))
+    record("block_quant_square", 4 * w.numel(),
+           lambda: zs.zero_block_quant(qw, ew, w, square=True, qt=qt, et=et))
+    y = torch.empty(tokens, hidden, dtype=bf16, device=dev)
+    ws = u8(zs.zero_block_product_workspace(tokens, hidden, width))
+    record("block_product", qx.numel() + qw.numel() + 2 * y.numel(),
+           lambda: zs.zero_block_product(y, qx, ex, qw, ew, workspace=ws),
+           2 * tokens * width * hidden)
+    del x, w, qx, ex, qw, ew, qt, et, ws
+    n = y.numel()
+    f, h = normal(tokens, hidden, 1.0, 43), torch.empty_like(y)
+    record("dropout", 4 * n, lambda: zs.zero_dropout(h, f, 0.1, 7, 8))
+    vec = [normal(1, hidden, 0.1, 44 + i)[0] for i in range(3)]
+    told = dict(post=zs.NORM_RMS, pre=zs.NORM_RMS, post_weight=vec[0], gate=vec[1],
+                pre_weight=vec[2], res_scale=0.5)
+    grads = [torch.empty(hidden, dtype=torch.float32, device=dev) for _ in range(3)]
+    ws = u8(zs.zero_residual_norm_workspace(tokens, hidden))
+    stats = torch.empty(tokens, 4, dtype=torch.float32, device=dev)
+    for name, dt in (("", bf16), ("_f32_stream", torch.float32)):
+        r, du = normal(tokens, hidden, 1.0, 47, dt), normal(tokens, hidden, 1e-2, 48, dt)
+        u, b = torch.empty_like(r), r.element_size()
+        record("residual_norm" + name, (4 + 2 * b) * n,
+               lambda: zs.zero_residual_norm(u, h, stats, r, f, **told))
+        record("residual_norm_backward" + name, (6 + 3 * b) * n,
+               lambda: zs.zero_residual_norm_backward(
+                   y, r, h, du, f, u, stats, d_post_weight=grads[0], d_gate=grads[1],
+                   d_pre_weight=grads[2], workspace=ws, **told))
+        del r, du, u
+    return out
+
+
 def measure_small(dev, steps: int = 300, warmup: int = 20) -> dict:
     """Whole-step time of the launch-bound workloads under three kinds of control.
 
@@ -711,7 +781,8 @@ def main():
                     help="timed steps of each configuration under 'workloads'")
     ap.add_argument("--extras", action="store_true",
                     help="also time the accumulate / FP32-gradient / device-control / exchange "
-                         "kernels on shards of --extras-elems elements and the gradient operators "
+                         "kernels on shards of --extras-elems elements and the gradient and block "
+                         "operators "
                          "(reported under 'extras')")
     ap.add_argument("--extras-elems", type=int, default=1 << 30,
                     help="shard size of the --extras measurements (elements)")
@@ -859,6 +930,7 @@ def main():
         log("[bench] extras ...")
         extras = measure_extras(dev, n_elem=args.extras_elems)
         extras["gradient_operators"] = measure_gradient_operators(dev)
+        extras["block_operators"] = measure_block_operators(dev)
 
     out = {
         "metric": METRIC,

@@ -922,36 +922,44 @@ __device__ __forceinline__ void put_grad(void *d, uint32_t col, float v, bool fi
         *t = from_f32<G>(v);
 }
 
-// The parts' four sums of a column, added in the parts' order by kJoinParts lanes (each its
-// share), those joined in order, and the gradients made from them.  G: the gradients' format.
+// The parts' four sums of a column: kJoinParts shares of the parts, each added in order by a
+// lane that has eight of them in flight, the shares joined in order, a lane a sum, and the
+// gradients made from them.  BIAS: all four sums are there, else the first and the third.
+// G: the gradients' format.
 constexpr uint32_t kJoinCols = 32, kJoinParts = 32;
-template <int F, int G>
+template <int F, int G, bool BIAS>
 __global__ __launch_bounds__(kJoinCols *kJoinParts) void join_grads_kernel(
-    Grads g, const float *__restrict__ part, uint32_t parts, uint32_t cols, bool bias_sums,
-    const void *w1, const void *b1, const void *gate) {
+    Grads g, const float *__restrict__ part, uint32_t parts, uint32_t cols, const void *w1,
+    const void *b1, const void *gate) {
     __shared__ float slots[4][kJoinParts][kJoinCols];
     const uint32_t lane_col = threadIdx.x % kJoinCols, share = threadIdx.x / kJoinCols;
     const uint32_t per = (parts + kJoinParts - 1) / kJoinParts;
+    const uint32_t from = share * per < parts ? share * per : parts;
+    const uint32_t to = from + per < parts ? from + per : parts;
     for (uint64_t c0 = static_cast<uint64_t>(blockIdx.x) * kJoinCols; c0 < cols;
          c0 += static_cast<uint64_t>(gridDim.x) * kJoinCols) {
         const uint64_t col = c0 + lane_col;
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (col < cols) {
-            const uint32_t from = share * per, to = from + per < parts ? from + per : parts;
-#pragma unroll 4
+#pragma unroll 8
             for (uint32_t k = from; k < to; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (bias_sums || i % 2 == 0)
-                        sum[i] = sum[i] + part[(static_cast<uint64_t>(k) * 4 + i) * cols + col];
+                for (int i = 0; i < 4; i += BIAS ? 1 : 2)
+                    sum[i] = sum[i] + part[(static_cast<uint64_t>(k) * 4 + i) * cols + col];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) slots[i][share][lane_col] = sum[i];
+        for (int i = 0; i < 4; i += BIAS ? 1 : 2) slots[i][share][lane_col] = sum[i];
+        __syncthreads();
+        if (share < 4 && (BIAS || share % 2 == 0)) {
+            float x = slots[share][0][lane_col];
+#pragma unroll
+            for (uint32_t k = 1; k < kJoinParts; ++k) x = x + slots[share][k][lane_col];
+            slots[share][0][lane_col] = x;
+        }
         __syncthreads();
         if (share == 0 && col < cols) {
-            for (uint32_t k = 1; k < kJoinParts; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum[i] = sum[i] + slots[i][k][lane_col];
+            for (int i = 0; i < 4; i += BIAS ? 1 : 2) sum[i] = slots[i][0][lane_col];
             const uint32_t c = static_cast<uint32_t>(col);
             float one[8], bias[8], gt[8];
             load_param<F>(w1, c, 1, 1.0f, one);
@@ -966,6 +974,17 @@ __global__ __launch_bounds__(kJoinCols *kJoinParts) void join_grads_kernel(
         }
         __syncthreads();
     }
+}
+
+template <int F, int G>
+void join_grads(const Grads &g, const ResidualArgs &a, const float *part, uint32_t parts,
+                bool bias_sums, uint32_t blocks, hipStream_t stream) {
+    if (bias_sums)
+        join_grads_kernel<F, G, true><<<blocks, kJoinCols * kJoinParts, 0, stream>>>(
+            g, part, parts, a.cols, a.w1, a.b1, a.gate);
+    else
+        join_grads_kernel<F, G, false><<<blocks, kJoinCols * kJoinParts, 0, stream>>>(
+            g, part, parts, a.cols, a.w1, a.b1, a.gate);
 }
 
 Step step_of(const ResidualArgs &a) {
@@ -1003,12 +1022,14 @@ constexpr Load load_of(bool bias_sums) {
     return R == 2 || bias_sums ? Load::kMiddle : Load::kLight;
 }
 
-// The backward pass: rows of one wave up to 1024 columns, so that a workgroup joins eight
-// rows' sums before it writes them; up to 8192 columns rows of several waves, one group a lane
+// The backward pass: rows of one wave up to 1024 columns, so that a workgroup joins eight rows'
+// sums before it writes them (1023 x 768 FP16, four sums: 19 us, in parts of four rows 22.6); up to 8192 columns rows of several waves, one group a lane
 // (16 waves of 128 registers), or two for what is heavy (8 of 256: 16384 x 8192 FP32, four
 // sums, 770 us against 844; 16-bit data with two sums: 378 against 348); up to 16384 columns
 // two groups of 16 waves for what is light (8192 x 12288 BF16: 355 us, walked over in memory
-// 607; with an FP32 stream 818 and 704).  As many parts as fill the chip once.
+// 607; with an FP32 stream 818 and 704).  As many parts as fill the chip once, fewer where a wave
+// would have less than four rows (each part is joined afterwards: 4000 x 512 FP16, four sums, 34
+// us in 500 parts, 24 in 256).
 RowPlan backward_plan(uint64_t rows, uint64_t cols, Load load) {
     const uint64_t per = (rows + kUnits - 1) / kUnits;
     RowPlan p{0, 1, 1, static_cast<uint32_t>((rows + per - 1) / per)};
@@ -1018,8 +1039,9 @@ RowPlan backward_plan(uint64_t rows, uint64_t cols, Load load) {
     p.waves = waves_of(cols, p.groups);
     if (p.waves == 1) p.at_once = static_cast<uint32_t>(rows < 8 ? rows : 8);
     const uint64_t resident = (p.groups == 1 ? 16 : 8) / (p.waves * p.at_once);
-    const uint64_t most = kUnits * (resident > 1 ? resident : 1);
+    uint64_t most = kUnits * (resident > 1 ? resident : 1);
     const uint64_t need = (rows + p.at_once - 1) / p.at_once;
+    while (most > kUnits && need < 4 * most) most = most / 2 > kUnits ? most / 2 : kUnits;
     p.parts = static_cast<uint32_t>(need < most ? need : most);
     return p;
 }
@@ -1106,11 +1128,9 @@ hipError_t backward_as(const ResidualArgs &a, hipStream_t stream) {
     if (!a.dw1 && !a.db1 && !a.dgate && !a.dw2 && !a.db2) return hipSuccess;
     const uint32_t blocks = capped((a.cols + kJoinCols - 1) / kJoinCols);
     if (a.grad32)
-        join_grads_kernel<F, 2><<<blocks, kJoinCols * kJoinParts, 0, stream>>>(
-            g, part, plan.parts, a.cols, bias_sums, a.w1, a.b1, a.gate);
+        join_grads<F, 2>(g, a, part, plan.parts, bias_sums, blocks, stream);
     else
-        join_grads_kernel<F, F><<<blocks, kJoinCols * kJoinParts, 0, stream>>>(
-            g, part, plan.parts, a.cols, bias_sums, a.w1, a.b1, a.gate);
+        join_grads<F, F>(g, a, part, plan.parts, bias_sums, blocks, stream);
     return hipGetLastError();
 }
 
