@@ -2,9 +2,11 @@
 //
 // The mask of eight neighbouring columns is one Philox4x32 block (ten rounds; Salmon,
 // Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011): 16 bits an
-// element, so that the generator costs a twelfth of a block's twenty multiplications an
-// element, below what the memory leaves time for.  16 bits put the probability on a grid of
-// 2^-16, which the factor of what stays goes by, so the mean is kept.
+// element, so that an element costs two and a half of the block's twenty wide products, which
+// run beside the memory's traffic.  16 bits put the probability on a grid of 2^-16, which the
+// factor of what stays goes by, so the mean is kept.
+//
+// Bound by HBM: BF16 16384 x 8192 87 us (6.2 TB/s), FP32 198 (5.4); FP16 61 x 769 the launch.
 #include "block_device.h"
 
 #pragma clang fp contract(off)

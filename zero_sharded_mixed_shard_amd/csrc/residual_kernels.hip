@@ -12,9 +12,10 @@
 // post norm's gate A and gate B.
 //
 // What bounds it: HBM, with the arithmetic close behind.  16384 x 8192, norms of the mean
-// square on both sides and a gate: BF16 with the stream in FP32 291 us forward and 477
-// backward (5.5 and 5.1 TB/s), all BF16 220 and 280 (4.9 and 5.8).  Rows walked over several
-// times in memory took 398 and 672.
+// square on both sides and a gate: all BF16 184 us forward and 274 backward (5.8 and 5.9
+// TB/s), the stream in FP32 294 and 469 (5.5 and 5.2).  Rows walked over several times in
+// memory took 367 and 672, and 398 and 965.  64 x 768 FP16: 5.5 us forward, the launch and two
+// sums; 1023 x 768 backward 15 and 4 for the join.
 //
 // Sums of squares are taken around the mean (two passes over a row that is on chip); rows
 // whose sum leaves FP32's middle are summed again scaled by 2^-80.
