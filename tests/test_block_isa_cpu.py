@@ -6,6 +6,7 @@ within a compute unit's, and the instructions the designs rest on.
 import importlib.util
 import os
 import re
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
@@ -21,7 +22,8 @@ def assembly():
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     assert set(SOURCES) <= set(mod.KERNEL_SOURCES)
-    return {src: mod.device_assembly(src) for src in SOURCES}
+    with ThreadPoolExecutor(len(SOURCES)) as pool:
+        return dict(zip(SOURCES, pool.map(mod.device_assembly, SOURCES)))
 
 
 def count(text, op):

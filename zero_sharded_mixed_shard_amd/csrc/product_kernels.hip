@@ -668,7 +668,8 @@ hipError_t product_as(const ProductArgs &a, hipStream_t stream) {
         return hipGetLastError();
     }
     if (p.splits == 1) return tiles_of<F, F != 2, false>(a, s, p, stream);
-    const hipError_t e = tiles_of<F, F != 2, true>(a, s, p, stream);
+    // (planes are FP32 whatever the format: one set of kernels for both 16-bit ones)
+    const hipError_t e = tiles_of<F == 0 ? 1 : F, F != 2, true>(a, s, p, stream);
     if (e != hipSuccess) return e;
     product_join_kernel<F><<<capped((a.m * a.n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
         y, a.ldy, static_cast<const float *>(a.workspace), a.m, a.n, p.splits);
