@@ -667,7 +667,8 @@ __global__ __launch_bounds__(64 * WAVES) void row_backward_kernel(
     constexpr bool kLong = V == 2 && WAVES == 16, kHeld = !kLong;
     __shared__ float slots[2][2][kRowWaves];
     __shared__ __align__(16) float kept[kLong ? 2 : 1][kLong ? kRowWaves * 1024 : 4];
-    extern __shared__ float joined[];   // [rows at once][cols], W == 1 only
+    // [rows at once][columns in whole groups], W == 1 only
+    extern __shared__ __align__(16) float joined[];
     RowTotal total(slots, waves);
     const MaskKey key(s.mask);
     const float cols = static_cast<float>(s.cols);
@@ -888,17 +889,25 @@ __global__ __launch_bounds__(64 * WAVES) void row_backward_kernel(
                                      kLong && k % 2 == 0 ? &kept[k / 2][mine.col(v)] : sums[k][v]);
                 continue;
             }
+            // (whole groups, in lines of whole groups)
+            const uint32_t line = (s.cols + 7) & ~7u;
             __syncthreads();
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j)
-                    if (j < mine.n(v))
-                        joined[total.wave * s.cols + mine.col(v) + j] = sums[k][v][j];
+            for (int v = 0; v < V; ++v) {
+                if (mine.n(v) == 0) continue;
+                f32x4 *t = reinterpret_cast<f32x4 *>(&joined[total.wave * line + mine.col(v)]);
+                t[0] = f32x4{sums[k][v][0], sums[k][v][1], sums[k][v][2], sums[k][v][3]};
+                t[1] = f32x4{sums[k][v][4], sums[k][v][5], sums[k][v][6], sums[k][v][7]};
+            }
             __syncthreads();
             for (uint32_t c = threadIdx.x; c < s.cols; c += blockDim.x) {
                 float x = joined[c];
-                for (uint32_t w = 1; w < at_once; ++w) x = x + joined[w * s.cols + c];
+                if (at_once == 8) {
+#pragma unroll
+                    for (uint32_t w = 1; w < 8; ++w) x = x + joined[w * line + c];
+                } else {
+                    for (uint32_t w = 1; w < at_once; ++w) x = x + joined[w * line + c];
+                }
                 d[c] = x;
             }
         }
@@ -1082,7 +1091,7 @@ template <int F, int R, bool BIAS>
 hipError_t rows_backward(const Step &s, const RowPlan &plan, const Back<F, R> &p, float *part,
                          hipStream_t stream) {
     const uint32_t threads = 64 * plan.waves * plan.at_once, grid = capped(plan.parts);
-    const size_t lds = plan.at_once > 1 ? sizeof(float) * plan.at_once * s.cols : 0;
+    const size_t lds = plan.at_once > 1 ? sizeof(float) * plan.at_once * ((s.cols + 7) & ~7u) : 0;
     constexpr Load kLoad = load_of<F, R>(BIAS);
 #define ZS_ROWS(V, WAVES)                                                                    \
     row_backward_kernel<F, R, V, WAVES, BIAS><<<grid, threads, lds, stream>>>(               \
