@@ -139,22 +139,19 @@ def zero_dropout(y: torch.Tensor, x: torch.Tensor, p: float, seed: int, offset: 
 
 # ---- the step between two blocks -----------------------------------------------------------
 
-def _optional(t, name: str, dtypes, shape, dev):
-    return None if t is None else _flat(t, name, dtypes, shape, dev)
-
-
 def _description(shape, dt, res_dt, dev, post, pre, post_weight, post_bias, gate, pre_weight,
                  pre_bias, eps, res_scale, p, seed, offset, d_offset) -> _Residual:
-    rows, cols = shape
-    dts, vec = (dt,), (cols,)
-    return _Residual(rows, cols, _FORMATS[dt], _FORMATS[res_dt], post, pre,
-                     _optional(post_weight, "post_weight", dts, vec, dev),
-                     _optional(post_bias, "post_bias", dts, vec, dev),
-                     _optional(gate, "gate", dts, vec, dev),
-                     _optional(pre_weight, "pre_weight", dts, vec, dev),
-                     _optional(pre_bias, "pre_bias", dts, vec, dev),
-                     eps, res_scale, p, seed, offset,
-                     _optional(d_offset, "d_offset", _I64, (1,), dev))
+    # (spelled out: this runs on every call)
+    dts, vec = (dt,), shape[1:]
+    return _Residual(
+        shape[0], shape[1], _FORMATS[dt], _FORMATS[res_dt], post, pre,
+        None if post_weight is None else _flat(post_weight, "post_weight", dts, vec, dev),
+        None if post_bias is None else _flat(post_bias, "post_bias", dts, vec, dev),
+        None if gate is None else _flat(gate, "gate", dts, vec, dev),
+        None if pre_weight is None else _flat(pre_weight, "pre_weight", dts, vec, dev),
+        None if pre_bias is None else _flat(pre_bias, "pre_bias", dts, vec, dev),
+        eps, res_scale, p, seed, offset,
+        None if d_offset is None else _flat(d_offset, "d_offset", _I64, (1,), dev))
 
 
 def _pointer(t, name: str, dtypes, shape, dev) -> tuple:
@@ -183,7 +180,7 @@ def zero_residual_norm(u: torch.Tensor | None, h: torch.Tensor | None,
     p_f, ldf = _pointer(f, "f", (dt,), shape, dev)
     p_h, ldh = _pointer(h, "h", (dt,), shape, dev)
     p_u, ldu = _pointer(u, "u", (res_dt,), shape, dev)
-    p_s = _optional(stats, "stats", _F32, (shape[0], 4), dev)
+    p_s = None if stats is None else _flat(stats, "stats", _F32, (shape[0], 4), dev)
     block = _description(shape, dt, res_dt, dev, post, pre, post_weight, post_bias, gate,
                          pre_weight, pre_bias, eps, res_scale, p, seed, offset, d_offset)
     _call("zero_residual_norm", lib.zero_residual_norm, dev, stream, p_u, ldu, p_h, ldh, p_s, p_r,
@@ -234,11 +231,11 @@ def zero_residual_norm_backward(df: torch.Tensor | None, dr: torch.Tensor,
     named = (("d_post_weight", d_post_weight), ("d_post_bias", d_post_bias), ("d_gate", d_gate),
              ("d_pre_weight", d_pre_weight), ("d_pre_bias", d_pre_bias))
     grad_dt, grads = dt, []
-    for name, t in named:
+    for _, t in named:
         if isinstance(t, torch.Tensor) and t.dtype == torch.float32:
             grad_dt = torch.float32
     for name, t in named:
-        grads.append(_optional(t, name, (grad_dt,), (shape[1],), dev))
+        grads.append(None if t is None else _flat(t, name, (grad_dt,), shape[1:], dev))
     p_ws, n_ws = _workspace(workspace, dev)
     _call("zero_residual_norm_backward", lib.zero_residual_norm_backward, dev, stream, p_df, lddf,
           p_dr, lddr, ctypes.byref(_ResidualGrads(*grads)), _FORMATS[grad_dt], int(bool(first)),
