@@ -15,7 +15,7 @@
 // square on both sides and a gate: all BF16 184 us forward and 274 backward (5.8 and 5.9
 // TB/s), the stream in FP32 294 and 469 (5.5 and 5.2).  Rows walked over several times in
 // memory took 367 and 672, and 398 and 965.  64 x 768 FP16: 5.5 us forward, the launch and two
-// sums; 1023 x 768 backward 15 and 4 for the join.
+// sums; 1023 x 768 backward 13 and 4 for the join.
 //
 // Sums of squares are taken around the mean (two passes over a row that is on chip); rows
 // whose sum leaves FP32's middle are summed again scaled by 2^-80.
@@ -1033,7 +1033,8 @@ constexpr Load load_of(bool bias_sums) {
 }
 
 // The backward pass: rows of one wave up to 1024 columns, so that a workgroup joins eight rows'
-// sums before it writes them (1023 x 768 FP16, four sums: 19 us, in parts of four rows 22.6); up to 8192 columns rows of several waves, one group a lane
+// sums before it writes them (1023 x 768 FP16, four sums: 17.4 us; in parts of four rows 22.6
+// where these took 19); up to 8192 columns rows of several waves, one group a lane
 // (16 waves of 128 registers), or two for what is heavy (8 of 256: 16384 x 8192 FP32, four
 // sums, 770 us against 844; 16-bit data with two sums: 378 against 348); up to 16384 columns
 // two groups of 16 waves for what is light (8192 x 12288 BF16: 355 us, walked over in memory
