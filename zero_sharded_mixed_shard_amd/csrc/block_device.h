@@ -32,6 +32,22 @@ __device__ __forceinline__ Raw8<F> raw_group(const elem_t<F> *row, uint32_t col,
     return load8<F>(row + (col + 8 <= cols ? col : cols - 8));
 }
 
+// Eight values of format F as raw bits.
+template <int F>
+__device__ __forceinline__ Raw8<F> narrow8(const float v[8]) {
+    Raw8<F> r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (F == 2) {
+            r.v[0][j] = bits(v[j]);
+            r.v[1][j] = bits(v[4 + j]);
+        } else {
+            r.v[0][j] = pack2<F>(v[2 * j], v[2 * j + 1]);
+        }
+    }
+    return r;
+}
+
 // What was read as the row's last eight, moved down to the n (1 to 7) that are the lane's,
 // zeros above.
 template <int F>

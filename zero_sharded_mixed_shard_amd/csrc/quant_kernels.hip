@@ -101,22 +101,6 @@ __global__ __launch_bounds__(kThreads) void quant_row_kernel(
     }
 }
 
-// Eight values of format F as raw bits.
-template <int F>
-__device__ __forceinline__ Raw8<F> narrow8(const float v[8]) {
-    Raw8<F> r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if constexpr (F == 2) {
-            r.v[0][j] = bits(v[j]);
-            r.v[1][j] = bits(v[4 + j]);
-        } else {
-            r.v[0][j] = pack2<F>(v[2 * j], v[2 * j + 1]);
-        }
-    }
-    return r;
-}
-
 // Four rows of four bytes as four columns.
 __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
                                            uint32_t out[4]) {

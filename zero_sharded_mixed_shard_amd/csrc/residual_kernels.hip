@@ -14,7 +14,7 @@
 // What bounds it: HBM, with the arithmetic close behind.  16384 x 8192, norms of the mean
 // square on both sides and a gate: all BF16 184 us forward and 274 backward (5.8 and 5.9
 // TB/s), the stream in FP32 294 and 469 (5.5 and 5.2).  Rows walked over several times in
-// memory took 367 and 672, and 398 and 965.  64 x 768 FP16: 5.5 us forward, the launch and two
+// memory took 367 and 672, and 398 and 965 (the latter before their requests stood a row ahead).  64 x 768 FP16: 5.5 us forward, the launch and two
 // sums; 1023 x 768 backward 13 and 4 for the join.
 //
 // Sums of squares are taken around the mean (two passes over a row that is on chip); rows
@@ -343,16 +343,34 @@ __global__ __launch_bounds__(kWideThreads) void wide_means_kernel(Step s, Back<F
     }
 }
 
+// The n (0 to 8) columns of a group that are the lane's, zeros past them; ragged: the row's
+// length is no multiple of eight.
+template <int F>
+__device__ __forceinline__ void widen_some(Raw8<F> &r, bool ragged, uint32_t n, float out[8]) {
+    if (ragged) {
+        if (n - 1u < 7u) move_down<F>(r, n);
+    }
+    if (n != 0) {
+        widen8<F>(r, out);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = 0.0f;
+    }
+}
+
 // df, dr and the four column sums over the rows of part blockIdx.y, to
-// part[blockIdx.y][4][cols].  A lane owns eight columns.  df may be dh, and dr du: a lane
-// reads its elements before it writes them.
-template <int F, int R>
+// part[blockIdx.y][4][cols].  A lane owns eight columns; the next row's are on their way while
+// it works on this one's (read without a branch where rows have eight columns at least, see
+// below).  df may be dh, and dr du: a lane reads its elements before it writes them.
+template <int F, int R, bool NARROW>
 __global__ __launch_bounds__(kWideThreads) void wide_backward_kernel(
     Step s, Back<F, R> p, const float *__restrict__ means, float *__restrict__ part,
     uint64_t rows_per_part) {
     const MaskKey key(s.mask);
     const uint64_t first = blockIdx.y * rows_per_part;
     const uint64_t last = first + rows_per_part < s.rows ? first + rows_per_part : s.rows;
+    const bool pre = s.pre != ZERO_NORM_NONE, post = s.post != ZERO_NORM_NONE;
+    const bool ragged = s.cols % 8 != 0;
     constexpr uint64_t kStride = kWideThreads * 8;
     for (uint64_t c = blockIdx.x * kStride + threadIdx.x * 8u; c < s.cols;
          c += gridDim.x * kStride) {
@@ -362,29 +380,68 @@ __global__ __launch_bounds__(kWideThreads) void wide_backward_kernel(
         load_param<F>(s.w1, col, n, 1.0f, w1);
         load_param<F>(s.w2, col, n, 1.0f, w2);
         load_param<F>(s.gate, col, n, 1.0f, gate);
+        Raw8<F> raw_dh, raw_f;
+        Raw8<R> raw_u, raw_du;
+        auto fetch = [&](uint64_t t) {
+            const elem_t<F> *dh = pre ? p.dh + t * p.lddh : p.f + t * p.ldf;
+            const elem_t<R> *u = pre ? p.u + t * p.ldu : p.du + t * p.lddu;
+            const elem_t<F> *f = p.f != nullptr ? p.f + t * p.ldf : dh;
+            const elem_t<R> *du = p.du != nullptr ? p.du + t * p.lddu : u;
+            if constexpr (!NARROW) {
+                raw_dh = raw_group<F>(dh, col, s.cols);
+                raw_u = raw_group<R>(u, col, s.cols);
+                raw_f = raw_group<F>(f, col, s.cols);
+                raw_du = raw_group<R>(du, col, s.cols);
+            } else {
+                float v[8];
+                load_some<F>(dh + col, n, v);
+                raw_dh = narrow8<F>(v);
+                load_some<R>(u + col, n, v);
+                raw_u = narrow8<R>(v);
+                load_some<F>(f + col, n, v);
+                raw_f = narrow8<F>(v);
+                load_some<R>(du + col, n, v);
+                raw_du = narrow8<R>(v);
+            }
+        };
+        if (first < last) fetch(first);
         for (uint64_t row = first; row < last; ++row) {
             const float *st = p.stats + row * 4, *mn = means + row * 4;
-            const RowMeans m{st[0], st[1], st[2], st[3], mn[0], mn[1], mn[2], mn[3]};
-            float dh[8], uhat[8], G[8], fhat[8], out[8];
-            pre8(p, row, col, n, m, dh, uhat);
-            stream8(p, row, col, n, m, dh, uhat, w2, G);
+            const float mean1 = st[0], rho1 = st[1], mean2 = st[2], rho2 = st[3];
+            const float zg2 = mn[0], g2 = mn[1], zg1 = mn[2], g1 = mn[3];
+            float dh[8], z[8], G[8], fh[8], out[8];
+            const bool move = ragged && !NARROW;
+            widen_some<F>(raw_dh, move, n, dh);
+            widen_some<R>(raw_u, move, n, z);
+            widen_some<F>(raw_f, move, n, fh);
+            widen_some<R>(raw_du, move, n, G);
+            fetch(row + 1 < last ? row + 1 : row);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                sums[0][j] = sums[0][j] + dh[j] * uhat[j];
-                sums[1][j] = sums[1][j] + dh[j];
+                if (p.du == nullptr) G[j] = 0.0f;
+                if (pre) {
+                    z[j] = (z[j] - mean2) * rho2;
+                    sums[0][j] = __builtin_fmaf(dh[j], z[j], sums[0][j]);
+                    sums[1][j] = sums[1][j] + dh[j];
+                    const float g = w2[j] * dh[j];
+                    G[j] = __builtin_fmaf(rho2, __builtin_fmaf(-zg2, z[j], g - g2), G[j]);
+                }
                 out[j] = product32(s.res_scale, G[j]);
             }
             if (p.f != nullptr) {
+                const uint32_t keep = s.mask.threshold != 0
+                                          ? key.keep8(static_cast<uint32_t>(row), col >> 3)
+                                          : 0xffu;
                 float df[8];
-                post8(s, key, p, row, col, n, m, G, fhat);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    sums[2][j] = sums[2][j] + G[j] * fhat[j];
+                    G[j] = (keep >> j) & 1u ? G[j] * s.mask.factor : 0.0f;
+                    if (post) fh[j] = (fh[j] - mean1) * rho1;
+                    sums[2][j] = __builtin_fmaf(G[j], fh[j], sums[2][j]);
                     sums[3][j] = sums[3][j] + G[j];
-                    const float x = gate[j] * G[j];
-                    df[j] = s.post == ZERO_NORM_NONE
-                                ? product32(gate[j], G[j])
-                                : product32(m.rho1, (w1[j] * x - m.g1) - fhat[j] * m.zg1);
+                    const float x = product32(gate[j], G[j]);
+                    df[j] = post ? product32(rho1, __builtin_fmaf(-zg1, fh[j], w1[j] * x - g1))
+                                 : x;
                 }
                 store_row<F>(p.df + row * p.lddf, col, n, df);
             }
@@ -392,10 +449,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_backward_kernel(
         }
         float *d = part + blockIdx.y * 4ull * s.cols + col;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                if (j < n) d[static_cast<uint64_t>(k) * s.cols + j] = sums[k][j];
+        for (int k = 0; k < 4; ++k) store_row<2>(d + static_cast<uint64_t>(k) * s.cols, 0, n, sums[k]);
     }
 }
 
@@ -412,21 +466,6 @@ __global__ __launch_bounds__(kWideThreads) void wide_backward_kernel(
 // and an operand that is not there is read from another one's place.
 
 constexpr int kRowWaves = 16;   // most waves of a workgroup
-
-// The n (0 to 8) columns of a group that are the lane's, zeros past them; ragged: the row's
-// length is no multiple of eight.
-template <int F>
-__device__ __forceinline__ void widen_some(Raw8<F> &r, bool ragged, uint32_t n, float out[8]) {
-    if (ragged) {
-        if (n - 1u < 7u) move_down<F>(r, n);
-    }
-    if (n != 0) {
-        widen8<F>(r, out);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) out[j] = 0.0f;
-    }
-}
 
 // Sums over a row's W waves, the same in every lane.  The waves' sums go through LDS, in two
 // halves in turn, so that one barrier a sum is enough; W == 1 needs neither.
@@ -1038,7 +1077,7 @@ constexpr Load load_of(bool bias_sums) {
 // (16 waves of 128 registers), or two for what is heavy (8 of 256: 16384 x 8192 FP32, four
 // sums, 770 us against 844; 16-bit data with two sums: 378 against 348); up to 16384 columns
 // two groups of 16 waves for what is light (8192 x 12288 BF16: 355 us, walked over in memory
-// 607; with an FP32 stream 818 and 704).  As many parts as fill the chip once, fewer where a wave
+// 607; with an FP32 stream 818 and 669).  As many parts as fill the chip once, fewer where a wave
 // would have less than four rows (each part is joined afterwards: 4000 x 512 FP16, four sums, 34
 // us in 500 parts, 24 in 256).
 RowPlan backward_plan(uint64_t rows, uint64_t cols, Load load) {
@@ -1127,8 +1166,13 @@ hipError_t backward_as(const ResidualArgs &a, hipStream_t stream) {
         if (e != hipSuccess) return e;
         const dim3 grid(capped((a.cols + kWideThreads * 8ull - 1) / (kWideThreads * 8ull)),
                         plan.parts);
-        wide_backward_kernel<F, R><<<grid, kWideThreads, 0, stream>>>(
-            s, p, means, part, (a.rows + plan.parts - 1) / plan.parts);
+        const uint64_t per = (a.rows + plan.parts - 1) / plan.parts;
+        if (a.cols < 8)
+            wide_backward_kernel<F, R, true><<<grid, kWideThreads, 0, stream>>>(s, p, means, part,
+                                                                                per);
+        else
+            wide_backward_kernel<F, R, false><<<grid, kWideThreads, 0, stream>>>(s, p, means, part,
+                                                                                 per);
         e = hipGetLastError();
     } else {
         e = bias_sums ? rows_backward<F, R, true>(s, plan, p, part, stream)
