@@ -81,7 +81,7 @@ int zero_block_load(void *x, uint64_t ldx, zero_dtype dt, const uint8_t *q, cons
  *       answer, 16-byte aligned; may be NULL if that is 0.  Its contents
  *       before the call do not matter.
  *   m == 0 or n == 0: no-op.  k == 0: y = 0.  k below 16, or of 2^24 and more,
- *   is correct but many times slower.
+ *   is summed in FP64, and many times slower.
  *   Errors: ZERO_EDTYPE; ZERO_EINVAL for an a_block other than those two, a
  *   NULL or misaligned pointer, ldy < n, a small or misaligned workspace, an
  *   extent past its limit, or an overlap; ZERO_EHIP.

@@ -526,8 +526,9 @@ __global__ __launch_bounds__(kThreads) void product_join_kernel(elem_t<F> *__res
     }
 }
 
-// One result a lane, element by element: for the few products whose rows are too short for
-// the tiles.
+// One result a lane, element by element: for the few products whose rows are too short or too
+// long for the tiles.  Summed in FP64, where products are exact and 2^31 of them lose nothing that
+// FP32 shows (a single FP32 sum of 2^24 ones and more stays at 2^24).
 template <int F>
 __global__ __launch_bounds__(kThreads) void product_plain_kernel(
     elem_t<F> *__restrict__ y, const uint8_t *__restrict__ qa, const uint8_t *__restrict__ ea,
@@ -536,14 +537,14 @@ __global__ __launch_bounds__(kThreads) void product_plain_kernel(
     for (uint64_t at = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x; at < total;
          at += static_cast<uint64_t>(gridDim.x) * kThreads) {
         const uint64_t i = at / s.n, j = at - i * s.n;
-        float sum = 0.0f;
+        double sum = 0.0;
         for (uint32_t c = 0; c < s.k; ++c) {
             const int e = static_cast<int>(ea[i * s.blocks_a + (c >> s.shift_a)]) +
                           static_cast<int>(eb[(j >> 7) * s.blocks_b + (c >> 7)]) - 254;
             const float p = code_value(qa[i * s.k + c]) * code_value(qb[j * s.k + c]);
-            sum = sum + __builtin_amdgcn_ldexpf(p, e);
+            sum = sum + __builtin_amdgcn_ldexp(static_cast<double>(p), e);
         }
-        y[i * s.ldy + j] = from_f32<F>(sum);
+        y[i * s.ldy + j] = from_f32<F>(static_cast<float>(sum));
     }
 }
 
