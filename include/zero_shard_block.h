@@ -72,7 +72,9 @@ int zero_block_load(void *x, uint64_t ldx, zero_dtype dt, const uint8_t *q, cons
  *   qa, ea  codes of a, exponents [m, ceil(k/a_block)], contiguous.  a_block
  *       is ZERO_BLOCK, or ZERO_ACT_BLOCK for an activation checkpoint.
  *   qb, eb  codes of b, exponents [ceil(n/128), ceil(k/128)], contiguous.
- *   Products are exact.  dt == ZERO_F32: summed in FP32.  16-bit dt: rounded
+ *   Products are exact.  dt == ZERO_F32: summed in FP32 (in FP64, and many times
+ *   slower, in tiles where a block has exponent byte 247, values of 1.75 * 2^127
+ *   and more).  16-bit dt: rounded
  *   once from FP32 sums whose matrix instructions drop, from each product of a
  *   group of eight, what lies 2^-13 and more below the group's largest (an
  *   error of at most 2^-10 of the sum of magnitudes, typically 1.5e-5 of the

@@ -76,6 +76,38 @@ def test_sums_of_whole_numbers_are_exact(m, n, k, a_block):
           eb.to(torch.uint8).contiguous(), a_block, 2.0 ** -4)
 
 
+@pytest.mark.parametrize("a_block", [128, 32])
+@pytest.mark.parametrize("m,n,k", [(2, 3, 12), (5, 40, 300), (65, 150, 4097), (2300, 2300, 300),
+                                   (3000, 4096, 640)])
+def test_the_smallest_numbers_against_the_largest(m, n, k, a_block):
+    # blocks whose exponent byte is 3 and whose codes are below the format's normal numbers (whole
+    # numbers of 2^-133), against blocks of byte 247 and codes up to 448; even blocks have the
+    # small side in a, odd ones in b
+    g = torch.Generator(device="cuda").manual_seed(m + n + k + a_block)
+    sign = lambda shape: (torch.randint(2, shape, generator=g, device=DEV) * 128).to(torch.uint8)
+    small = lambda rows: (torch.randint(8, (rows, k), generator=g, device=DEV) * 2 +
+                          1).to(torch.uint8) | sign((rows, k))
+    big = lambda rows: as_codes(torch.tensor(
+        [1.0, -3.0, 7.0, 30.0, 448.0, -256.0], device=DEV)[torch.randint(
+            6, (rows, k), generator=g, device=DEV)])
+    nb = -(-k // 128)
+    even = torch.arange(nb, device=DEV) % 2 == 0
+    cols = even.repeat_interleave(128)[:k]
+    qa = torch.where(cols, small(m), big(m))
+    qb = torch.where(cols, big(n), small(n))
+    ea = torch.where(even, 3, 247).to(torch.uint8).expand(m, -1).clone()
+    eb = torch.where(even, 247, 3).to(torch.uint8).expand(-(-n // 128), -1).clone()
+    # rows of a whose first block has the largest scale as well: its only code that is not zero
+    # meets zeros of b, so that the block adds nothing (and no infinity)
+    qa[1::3, :128] = 0
+    qa[1::3, 1] = 0x7e
+    qb[:, 1] = 0
+    ea[1::3, 0] = 247
+    if a_block == 32:
+        ea = ea.repeat_interleave(4, 1)[:, :-(-k // 32)].contiguous()
+    check(qa, ea, qb, eb, a_block, 2.0 ** -13)
+
+
 def test_rows_of_the_largest_scale_on_both_sides():
     # byte 247 on either side and on both (there a's codes are zeros: an infinity made of b's
     # would give NaN), in some rows of a tile and not in others

@@ -16,7 +16,7 @@
 // BF16: busy in 64% of 8.2e5 cycles, 447 us, 2.46 PFLOP/s; the library's FP8 product 400), and
 // between a workgroup's tiles their results, which all compute units store at once (16384 x
 // 8192 x 4096: 455 us on weights and hidden states, 540 on codes of full spread; library 446).
-// FP32 results of the latter 902 us (1.22 PFLOP/s).  1 x 8192 x 8192 15.6 us (4.3 TB/s of codes),
+// FP32 results of the latter 860 us (1.28 PFLOP/s).  1 x 8192 x 8192 15.6 us (4.3 TB/s of codes),
 // 61 x 50257 x 768 FP32 13, the call from the host included.
 //
 // LDS rows are 128 B, half the banks; 16-B unit c of row r lies at unit c ^ (r / 2 mod 8), so
@@ -68,11 +68,16 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t lo, uint32_t hi, float 
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// Half the scale of an exponent byte: a code of 448 under the largest scale is past BF16's
-// range, its half is not.  Sums of such products are multiplied by 4 at the end (kUnhalve).
-// Of what a code stands for only 2^-133, the smallest, is lost.
-__device__ __forceinline__ float half_scale(uint32_t e) { return from_bits((e - 1u) << 23); }
-constexpr float kUnhalve = 4.0f;
+// The scale of an exponent byte below the largest: BF16 holds all that a code stands for under
+// it, from 2^-133, its smallest number, on.  Codes of 256 and more under the largest byte are
+// past its end: results that such blocks have a part in are made element by element (see
+// store_plain).
+constexpr uint32_t kTopByte = 247;
+__device__ __forceinline__ float bf16_scale(uint32_t e) { return from_bits(e << 23); }
+// Not zero: some byte of a word is 247 or more (bit 7 is set, and the rest is 119 or more).
+__device__ __forceinline__ uint32_t top_bytes(uint32_t w) {
+    return ((w & 0x7f7f7f7fu) + 0x09090909u) & w & 0x80808080u;
+}
 
 // Order of a scheduling region that holds M MFMAs, R LDS reads, W LDS writes and G memory
 // reads: each kind dealt evenly between the MFMAs.
@@ -108,6 +113,23 @@ struct ProductShape {
     uint64_t work;                 // tiles, along n first (grouped by XCD they took the same time)
 };
 
+// Columns c0 to c1 of one result.  Summed in FP64, where products are exact and 2^31 of them lose
+// nothing that FP32 shows (a single FP32 sum of 2^24 ones and more stays at 2^24).
+__device__ __forceinline__ float plain_sum(const uint8_t *__restrict__ qa,
+                                           const uint8_t *__restrict__ ea,
+                                           const uint8_t *__restrict__ qb,
+                                           const uint8_t *__restrict__ eb, const ProductShape &s,
+                                           uint64_t i, uint64_t j, uint32_t c0, uint32_t c1) {
+    double sum = 0.0;
+    for (uint32_t c = c0; c < c1; ++c) {
+        const int e = static_cast<int>(ea[i * s.blocks_a + (c >> s.shift_a)]) +
+                      static_cast<int>(eb[(j >> 7) * s.blocks_b + (c >> 7)]) - 254;
+        const float p = code_value(qa[i * s.k + c]) * code_value(qb[j * s.k + c]);
+        sum = sum + __builtin_amdgcn_ldexp(static_cast<double>(p), e);
+    }
+    return static_cast<float>(sum);
+}
+
 // BM x BN tiles of y (or, SPLIT, of a split's FP32 plane); WM x WN waves.  EIGHT: the 8-bit
 // instruction.  A32: a's blocks are of 32 columns.  RAGGED: the last step is short.  Rows past the matrix are read as its last
 // one and not stored; columns past it are zeros.  k >= 16, and a tile's rows span less than
@@ -116,7 +138,7 @@ struct ProductShape {
 // b's rows are the matrix instruction's rows and a's its columns, so that a lane holds four
 // neighbours of a row of y.
 template <int F, bool EIGHT, bool SPLIT, bool A32, bool RAGGED, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_kernel(
+__global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : BM == 64 && !EIGHT ? 4 : 2) void product_tile_kernel(
     void *__restrict__ y, const uint8_t *__restrict__ qa, const uint8_t *__restrict__ ea,
     const uint8_t *__restrict__ qb, const uint8_t *__restrict__ eb, ProductShape s) {
     constexpr int kLanes = 64 * WM * WN;
@@ -333,7 +355,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
                                 b[TN == 1 ? kk : j], a[kk][i], acc[i][j], 0, 0, 0,
                                 static_cast<int>(wb), kk * 2, static_cast<int>(wa[i]));
                 } else {
-                    const float scale_b = half_scale(wb);
+                    const float scale_b = bf16_scale(wb);
     #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         bf16x8 d[TM];
@@ -341,7 +363,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
                         for (int i = 0; i < TM; ++i)
                             d[i] = codes_to_bf16(static_cast<uint32_t>(a[kk][i][2 * q]),
                                                  static_cast<uint32_t>(a[kk][i][2 * q + 1]),
-                                                 half_scale((wa[i] >> (8 * (kk * 2 + q / 2))) & 0xffu));
+                                                 bf16_scale((wa[i] >> (8 * (kk * 2 + q / 2))) & 0xffu));
     #pragma unroll
                         for (int j = from; j < to; ++j) {
                             const i32x8 &v = b[TN == 1 ? kk : j];
@@ -396,12 +418,24 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        // of this lane's rows of a: A32, not zero where a block has the largest byte; else their
+        // largest word (four times a byte); and the largest byte of b's blocks
+        uint32_t top = 0, top_b = 0;
 #pragma unroll 1
         for (uint32_t at = s0; at < s1; ++at) {
             trim();
             advance();   // (up here: with a branch behind them the products are moved past it)
             wb = eb_next;
             eb_next = xeb;
+            if constexpr (!EIGHT) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    if constexpr (A32)
+                        top |= top_bytes(wa[i]);
+                    else
+                        top = wa[i] > top ? wa[i] : top;
+                top_b = wb > top_b ? wb : top_b;
+            }
             if constexpr (TN > 1) read_b(H, TN, buf, 0);
             read_a(1, buf, 1);
             if constexpr (TN == 1) read_b(0, 1, buf, 1);
@@ -457,6 +491,21 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
                        (SPLIT ? blockIdx.y * (static_cast<uint64_t>(s.m) * s.n) : 0ull);
         const uint64_t ld = SPLIT ? s.n : s.ldy;
         const uint32_t turn = (row32 & kMask) * 2;
+        // store_plain: what a block of the largest byte makes of a sum may be past FP32
+        if constexpr (!EIGHT) {
+            if (__any((A32 ? top != 0 : top >> 24 >= kTopByte) || top_b >= kTopByte)) {
+                const uint32_t end = s1 * kStep < s.k ? s1 * kStep : s.k;
+#pragma unroll 1
+                for (uint32_t at = lane; at < BM / WM * W; at += 64) {
+                    const uint32_t row = tile.i0 + am + at / W, col = tile.j0 + bn + at % W;
+                    if (row < s.m && col < n)
+                        out[row * ld + col] =
+                            from_f32<F>(plain_sum(qa, ea, qb, eb, s, row, col, s0 * kStep, end));
+                }
+                if constexpr (!CHAIN) __syncthreads();   // the next tile writes LDS
+                continue;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -469,7 +518,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : 2) void product_tile_
                         float v[4];
 #pragma unroll
                         for (uint32_t t = 0; t < 4; ++t)
-                            v[t] = EIGHT ? acc[i][j][r + t] : acc[i][j][r + t] * kUnhalve;
+                            v[t] = acc[i][j][r + t];
                         if constexpr (kBytes == 2)
                             *reinterpret_cast<u32x2 *>(mine + row32 * (kPart * 2) + u * 8) =
                                 u32x2{pack2<F>(v[0], v[1]), pack2<F>(v[2], v[3])};
@@ -527,8 +576,7 @@ __global__ __launch_bounds__(kThreads) void product_join_kernel(elem_t<F> *__res
 }
 
 // One result a lane, element by element: for the few products whose rows are too short or too
-// long for the tiles.  Summed in FP64, where products are exact and 2^31 of them lose nothing that
-// FP32 shows (a single FP32 sum of 2^24 ones and more stays at 2^24).
+// long for the tiles.
 template <int F>
 __global__ __launch_bounds__(kThreads) void product_plain_kernel(
     elem_t<F> *__restrict__ y, const uint8_t *__restrict__ qa, const uint8_t *__restrict__ ea,
@@ -537,14 +585,7 @@ __global__ __launch_bounds__(kThreads) void product_plain_kernel(
     for (uint64_t at = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x; at < total;
          at += static_cast<uint64_t>(gridDim.x) * kThreads) {
         const uint64_t i = at / s.n, j = at - i * s.n;
-        double sum = 0.0;
-        for (uint32_t c = 0; c < s.k; ++c) {
-            const int e = static_cast<int>(ea[i * s.blocks_a + (c >> s.shift_a)]) +
-                          static_cast<int>(eb[(j >> 7) * s.blocks_b + (c >> 7)]) - 254;
-            const float p = code_value(qa[i * s.k + c]) * code_value(qb[j * s.k + c]);
-            sum = sum + __builtin_amdgcn_ldexp(static_cast<double>(p), e);
-        }
-        y[i * s.ldy + j] = from_f32<F>(static_cast<float>(sum));
+        y[i * s.ldy + j] = from_f32<F>(plain_sum(qa, ea, qb, eb, s, i, j, 0, s.k));
     }
 }
 
