@@ -132,3 +132,30 @@ def test_more_columns_than_fp32_counts():
         y = torch.zeros(1, 1, dtype=dt, device=DEV)
         zs.zero_block_product(y, q[:1], e[:1], q[1:], e[1:])
         assert float(y) == float(torch.tensor(float(k)).to(dt))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("a_block", [128, 32])
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_16_bit_results_lose_nothing_of_products_of_like_size(m, n, k, a_block, dt):
+    # whole products of 1 to 2^12: none has a part below 2^-13 of another, so that the 8-bit
+    # instruction's sums are exact as well and the one rounding is all that is left
+    g = torch.Generator(device="cuda").manual_seed(m + n + k + a_block)
+    pick = lambda shape, *v: torch.tensor(v, device=DEV)[
+        torch.randint(len(v), shape, generator=g, device=DEV)]
+    a = pick((m, k), -3.0, -2.0, -1.0, 1.0, 5.0, 13.0, 64.0, -60.0, 0.0)
+    b = pick((n, k), -7.0, -3.0, -1.0, 1.0, 2.0, 15.0, -64.0, 48.0)
+    d = torch.randint(-110, 111, (-(-k // 128),), generator=g, device=DEV)
+    ea = (121 + d).expand(m, -1)        # quanta of 2^-12, results within FP16's range
+    if a_block == 32:
+        ea = ea.repeat_interleave(4, 1)[:, :-(-k // 32)]
+    ea = ea.to(torch.uint8).contiguous()
+    eb = (121 - d).expand(-(-n // 128), -1).to(torch.uint8).contiguous()
+    qa, qb = as_codes(a), as_codes(b)
+    av, bv = values(qa, ea, a_block, 1), values(qb, eb, 128, 128)
+    want, mag = av @ bv.t().contiguous(), av.abs() @ bv.abs().t().contiguous()
+    assert float(mag.max()) < 2.0 ** 24 * 2.0 ** -12
+    y = torch.full((m, n), 99.0, device=DEV, dtype=dt)
+    zs.zero_block_product(y, qa, ea, qb, eb,
+                          workspace=u8(zs.zero_block_product_workspace(m, n, k)))
+    assert torch.equal(y, want.float().to(dt))
