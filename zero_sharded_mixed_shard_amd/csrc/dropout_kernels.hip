@@ -6,7 +6,7 @@
 // run beside the memory's traffic.  16 bits put the probability on a grid of 2^-16, which the
 // factor of what stays goes by, so the mean is kept.
 //
-// Bound by HBM: BF16 16384 x 8192 87 us (6.2 TB/s), FP32 198 (5.4); FP16 61 x 769 the launch.
+// Bound by HBM: BF16 16384 x 8192 89 us (6.1 TB/s), FP32 198 (5.4); FP16 61 x 769 the launch.
 #include "block_device.h"
 
 #pragma clang fp contract(off)

@@ -13,11 +13,13 @@
 // way from LDS and use the BF16 instruction, whose products are exact and whose sums are FP32.
 //
 // What bounds the large tiles: the matrix cores, at the clock that their power leaves (8192^3
-// BF16: busy in 64% of 8.2e5 cycles, 447 us, 2.46 PFLOP/s; the library's FP8 product 400), and
-// between a workgroup's tiles their results, which all compute units store at once (16384 x
-// 8192 x 4096: 455 us on weights and hidden states, 540 on codes of full spread; library 446).
-// FP32 results of the latter 860 us (1.28 PFLOP/s).  1 x 8192 x 8192 15.6 us (4.3 TB/s of codes),
-// 61 x 50257 x 768 FP32 13, the call from the host included.
+// BF16: busy in 64% of the cycles, 425 us, 2.59 PFLOP/s), and between a workgroup's tiles their
+// results, which all compute units store at once (16384 x 8192 x 4096: 448 us, 2.45 PFLOP/s).
+// These are means over calls in a row; the first twenty after an idle time take 460 to 650 while
+// the clock settles, so that the mean of sixty from there is 483.  Codes of full spread take 2%
+// longer.  The library's FP8 product, in turn with these on one card: 340 and 365 us.  FP32
+// results of the latter extents 883 us (1.25 PFLOP/s).  1 x 8192 x 8192 15.6 us (4.3 TB/s of
+// codes), 61 x 50257 x 768 FP32 13.
 //
 // LDS rows are 128 B, half the banks; 16-B unit c of row r lies at unit c ^ (r / 2 mod 8), so
 // that the rows which lanes read at once fall on different banks.
@@ -131,14 +133,15 @@ __device__ __forceinline__ float plain_sum(const uint8_t *__restrict__ qa,
 }
 
 // BM x BN tiles of y (or, SPLIT, of a split's FP32 plane); WM x WN waves.  EIGHT: the 8-bit
-// instruction.  A32: a's blocks are of 32 columns.  RAGGED: the last step is short.  Rows past the matrix are read as its last
-// one and not stored; columns past it are zeros.  k >= 16, and a tile's rows span less than
-// 4 GiB (the launcher checks both).
+// instruction.  A32: a's blocks are of 32 columns.  RAGGED: the last step is short.  Rows past
+// the matrix are read as its last one and not stored; columns past it are zeros.  k >= 16, and a
+// tile's rows span less than 4 GiB (the launcher checks both).
 //
 // b's rows are the matrix instruction's rows and a's its columns, so that a lane holds four
 // neighbours of a row of y.
 template <int F, bool EIGHT, bool SPLIT, bool A32, bool RAGGED, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : BM == 64 && !EIGHT ? 4 : 2) void product_tile_kernel(
+__global__ __launch_bounds__(64 * WM * WN, BM == 256 ? 1 : BM == 64 && !EIGHT ? 4 : 2)
+void product_tile_kernel(
     void *__restrict__ y, const uint8_t *__restrict__ qa, const uint8_t *__restrict__ ea,
     const uint8_t *__restrict__ qb, const uint8_t *__restrict__ eb, ProductShape s) {
     constexpr int kLanes = 64 * WM * WN;
@@ -626,10 +629,13 @@ constexpr TileCost kTiles[3] = {
     {256, 1, 1500, 1500, 9000}, {128, 2, 620, 500, 4000}, {64, 4, 400, 240, 3000}};
 
 // The tile and splits of least estimated time; splits cost the join's launch and its planes,
-// written and read.  Over nine shapes of 1 to 2048 rows, 768 to 50257 columns and 768 to 8192
-// summed ones the choice was within 10% of the best of every tile with 1 to 16 splits: 1024 x
-// 1024 x 8192, for example, takes 24 us in 128 x 128 tiles and 4 splits, 46 in one, 34 in 64 x
-// 64 tiles and 38 in 256 x 256 and 8 splits; 1 x 8192 x 8192 15.6 us in 64 x 64 and 4, 30 in one.
+// written and read.  The costs are those of 16-bit results; FP32 ones, whose steps take longer,
+// share them.  Over ten shapes of 1 to 2048 rows, 768 to 50257 columns and 768 to 8192 summed
+// ones the choice was within 5% of the best of every tile with 1 to 16 splits, for either kind of
+// results, but for 16 x 4096 x 4096 (8 splits: 10.0 us, FP32 11.0; 4 splits: 8.3 and 9.7).
+// 1024 x 1024 x 8192, for example, takes 24 us in 128 x 128 tiles and 4 splits (FP32 28), 28 in
+// 64 x 64 and 2 (FP32 32), 38 in 256 x 256 and 8; 1 x 8192 x 8192 15.6 us in 64 x 64 and 4 (FP32
+// 18), 30 in one.
 Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
     const uint64_t steps = (k + kStep - 1) / kStep;
     Plan best{0, 1, 0};

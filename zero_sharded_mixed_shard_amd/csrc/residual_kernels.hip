@@ -12,10 +12,12 @@
 // post norm's gate A and gate B.
 //
 // What bounds it: HBM, with the arithmetic close behind.  16384 x 8192, norms of the mean
-// square on both sides and a gate: all BF16 184 us forward and 274 backward (5.8 and 5.9
-// TB/s), the stream in FP32 294 and 469 (5.5 and 5.2).  Rows walked over several times in
-// memory took 367 and 672, and 398 and 965 (the latter before their requests stood a row ahead).  64 x 768 FP16: 5.5 us forward, the launch and two
-// sums; 1023 x 768 backward 13 and 4 for the join.
+// square on both sides and a gate, means over calls in a row: all BF16 172 to 199 us forward in
+// different runs (6.2 to 5.4 TB/s) and 274 backward (5.9), the stream in FP32 293 and 464 (5.5
+// and 5.2); all FP32 415 and 630 (5.2 and 5.1).  Rows walked over several times in memory took
+// 367 and 672, and 398 and 965 (the latter before their requests stood a row ahead); rows past
+// 16384 columns still are (4096 x 20480 BF16 212 and 446, half and a third of HBM's rate).  64 x
+// 768 FP16: 5.5 us forward, the launch and two sums; 1023 x 768 backward 13 and 4 for the join.
 //
 // Sums of squares are taken around the mean (two passes over a row that is on chip); rows
 // whose sum leaves FP32's middle are summed again scaled by 2^-80.
@@ -1073,13 +1075,15 @@ constexpr Load load_of(bool bias_sums) {
 
 // The backward pass: rows of one wave up to 1024 columns, so that a workgroup joins eight rows'
 // sums before it writes them (1023 x 768 FP16, four sums: 17.4 us; in parts of four rows 22.6
-// where these took 19); up to 8192 columns rows of several waves, one group a lane
-// (16 waves of 128 registers), or two for what is heavy (8 of 256: 16384 x 8192 FP32, four
-// sums, 770 us against 844; 16-bit data with two sums: 378 against 348); up to 16384 columns
-// two groups of 16 waves for what is light (8192 x 12288 BF16: 355 us, walked over in memory
-// 607; with an FP32 stream 818 and 669).  As many parts as fill the chip once, fewer where a wave
-// would have less than four rows (each part is joined afterwards: 4000 x 512 FP16, four sums, 34
-// us in 500 parts, 24 in 256).
+// where these took 19); up to 8192 columns rows of several waves, one group a lane (16 waves of
+// 128 registers), or two for what is heavy (8 of 256: 16384 x 8192 FP32, four sums, 652 us
+// against 948, two sums 630 against 728).  For the rest the two were alike when this was chosen;
+// at 16384 x 8192 one group now takes 276 us and two 278 where it is light, 471 and 458 with an
+// FP32 stream, 309 and 284 with four sums and a mask.  Up to 16384 columns two groups of 16
+// waves for what is light (8192 x 12288 BF16: 340 us, walked over in memory 494; with a mask 465
+// and 506; 8193 columns 362 and 416); the rest spills there (with an FP32 stream 818, walked over
+// 669).  As many parts as fill the chip once, fewer where a wave would have less than four rows
+// (each part is joined afterwards: 4000 x 512 FP16, four sums, 34 us in 500 parts, 24 in 256).
 RowPlan backward_plan(uint64_t rows, uint64_t cols, Load load) {
     const uint64_t per = (rows + kUnits - 1) / kUnits;
     RowPlan p{0, 1, 1, static_cast<uint32_t>((rows + per - 1) / per)};
