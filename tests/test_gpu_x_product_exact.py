@@ -37,10 +37,15 @@ def check(qa, ea, qb, eb, a_block, quantum):
     a, b = values(qa, ea, a_block, 1), values(qb, eb, 128, 128)
     want, mag = a @ b.t().contiguous(), a.abs() @ b.abs().t().contiguous()
     assert float(mag.max()) < 2.0 ** 24 * quantum
-    y = torch.full((m, n), 99.0, device=DEV)
-    zs.zero_block_product(y, qa, ea, qb, eb,
-                          workspace=u8(zs.zero_block_product_workspace(m, n, k)))
-    assert torch.equal(y.double(), want)
+    for cap in (0, 5):                  # 5: a workgroup's tiles one after another
+        y = torch.full((m, n), 99.0, device=DEV)
+        zs.zero_set_grid_cap(cap)
+        try:
+            zs.zero_block_product(y, qa, ea, qb, eb,
+                                  workspace=u8(zs.zero_block_product_workspace(m, n, k)))
+        finally:
+            zs.zero_set_grid_cap(0)
+        assert torch.equal(y.double(), want)
 
 
 # 64 x 64 tiles, whole and in splits (the third, fourth and fifth), 128 x 128 ones, whole and
